@@ -501,6 +501,63 @@ NVFP4_API nvfp4_status_t moe_ffn_forward_ex(const void* x_bf16, const float* log
                                   nvfp4_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------------
+ * nvfp4_linear_w4a16 — out = x W^T with NVFP4 weights and the activations as they are, for few
+ * rows: one launch that reads the weights once.
+ *
+ * nvfp4_linear quantizes its activations to 4 bits, which costs accuracy and, for a handful of
+ * rows, launches that take longer than the weights' transfer.  This call multiplies the same
+ * stored weights with bf16 activations: every decoded weight is exact, products are summed in
+ * FP32, the result is rounded once.
+ *
+ *   x         bf16 [M][ld] (ld >= K, ld % 8 == 0), any M >= 0.  Blocks of 32 rows each read the
+ *             weights again: meant for up to a few dozen rows
+ *   w, sfw    NVFP4 [N][K] (codes [N][K/2], tiled scales), gs_w device float[1]
+ *   out       [M][N], out_dtype 0 = float32, 1 = bf16:
+ *             out[m][n] = sum_k x[m][k] * E2M1(w[n][k]) * E4M3(sfw[n][k/16]) / gs_w
+ *   Infinities and NaNs of x reach the outputs of their own row only.  Results do not depend on
+ *   M or on the other rows' values except through the summation order, which M, N, K and the
+ *   device's SM count fix (the result is reproducible).
+ *   Constraints: K % 64 == 0, any N >= 1, M <= 2,097,120.
+ * ------------------------------------------------------------------------------------------- */
+NVFP4_API nvfp4_status_t nvfp4_linear_w4a16(const void* x, int64_t M, int K, int64_t ld,
+                                            const uint8_t* w, const uint8_t* sfw,
+                                            const float* gs_w, int N, void* out, int out_dtype,
+                                            nvfp4_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * moe_ffn_w4a16 — the expert FFN of a small batch with neither the activations nor the
+ * intermediate quantized: route, L1 with SwiGLU, L2, weighted sum, each chosen expert's weights
+ * read once (once per 8, 16 or 32 of its tokens).
+ *
+ * moe_ffn_forward's result without the two 4-bit roundings of x and h, from the same stored
+ * weights, and the faster form at a decode step: nothing is padded to 128 rows.
+ *
+ *   h_s = silu(g) * u, (g, u) = W1_e x_t (e = expert of slot s = t*k + j), kept in FP32;
+ *   out[t] = bf16( sum over live j of w_tj * W2_e h_s ), added in slot order (reproducible)
+ *
+ *   x_bf16    bf16 [T][H]
+ *   logits    float [T][E]: routed as in moe_permute (renormalized), and topk_ids and topk_w are
+ *             NULL; or NULL with
+ *   topk_ids  int32 [T][k] (< 0: dropped slot; >= E sets NVFP4_DEVERR_BAD_INDEX and is dropped)
+ *   topk_w    float [T][k], not read for dropped slots
+ *   w1, sfw1, gs_w1  NVFP4 [E*2I][H] in the gate/up interleave of moe_w1_row_map, float[E]
+ *   w2, sfw2, gs_w2  NVFP4 [E*H][I], float[E]
+ *   out_bf16  bf16 [T][H]; a token whose slots are all dropped gets zeros
+ *   ws        device scratch of moe_ffn_w4a16_workspace_size() bytes, 256-byte aligned
+ *   Constraints: H % 128 == 0, I % 64 == 0, 1 <= k <= E <= 256, k <= 32,
+ *   T*k <= NVFP4_W4A16_MAX_SLOTS (larger batches: moe_ffn_forward).
+ * ------------------------------------------------------------------------------------------- */
+#define NVFP4_W4A16_MAX_SLOTS 4096
+NVFP4_API size_t moe_ffn_w4a16_workspace_size(int T, int H, int I, int E, int k);
+NVFP4_API nvfp4_status_t moe_ffn_w4a16(const void* x_bf16, const float* logits,
+                                       const int32_t* topk_ids, const float* topk_w, int T, int H,
+                                       int I, int E, int k, const uint8_t* w1,
+                                       const uint8_t* sfw1, const float* gs_w1, const uint8_t* w2,
+                                       const uint8_t* sfw2, const float* gs_w2, void* out_bf16,
+                                       void* ws, size_t ws_bytes, int32_t* dev_status,
+                                       nvfp4_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
  * Status helpers.
  *   nvfp4_read_status: copies *dev_status to *host_code (host pointer) on `stream` and waits for
  *   the stream; returns NVFP4_ERR_TIMEOUT / NVFP4_ERR_BAD_INDEX when the matching bit is set.

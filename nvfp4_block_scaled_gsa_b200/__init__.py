@@ -16,8 +16,11 @@ from .api import (  # noqa: F401
     l2_scatter,
     l2_scatter_add,
     linear,
+    linear_w4a16,
     linear_workspace_bytes,
     moe_ffn_forward,
+    moe_ffn_w4a16,
+    moe_ffn_w4a16_workspace_bytes,
     mxfp4_grouped_gemm,
     mxfp4_quantize,
     moe_ffn_forward_ex,

@@ -154,10 +154,10 @@ def quantize_weights(get_expert, E, N, K, device="cuda", row_map=None):
     """Pre-pack expert weights: get_expert(e) -> bf16 (N, K) on the device; each expert gets its
     own global scale from its amax.  row_map (device int32 [N]): stored row of each row."""
     codes = torch.empty(E * N, K // 2, dtype=U8, device=device)
-    sf = torch.empty(E * N * K // 16, dtype=U8, device=device)
+    per_sf = sf_bytes(N, K)  # whole 128-row atoms: N need not be a multiple of 128
+    sf = torch.empty(E * per_sf, dtype=U8, device=device)
     gs = torch.empty(E, dtype=F32, device=device)
     ws = torch.empty(int(lib().nvfp4_quantize_workspace_size()), dtype=U8, device=device)
-    per_sf = N * K // 16
     for e in range(E):
         w = get_expert(e)
         assert w.dtype == BF16 and tuple(w.shape) == (N, K)
@@ -353,6 +353,88 @@ def moe_ffn_forward_ex(x, logits, k, w1: NVFP4Weights, w2: NVFP4Weights, gs_h, d
          _p(w1.gs), _p(w2.codes), _p(w2.sf), _p(w2.gs), _p(gs_h),
          (FFN_DELAYED_GS_H if delayed else 0) | (FFN_DETERMINISTIC if deterministic else 0),
          _p(h_stats), _p(out), _p(ws), ws.numel(), _p(status), _stream())
+    return out
+
+
+def _on_device(t):
+    """Context that makes t's device current (a no-op when it is)."""
+    assert t.is_cuda
+    return torch.cuda.device(t.device)
+
+
+def _check_on(dev, **tensors):
+    for name, t in tensors.items():
+        assert t is None or t.device == dev, f"{name} is not on {dev}"
+
+
+def _check_weights(w: "NVFP4Weights", dev):
+    """The buffers of w as the kernels index them."""
+    _check_on(dev, codes=w.codes, sf=w.sf, gs=w.gs)
+    assert w.codes.dtype == U8 and w.codes.is_contiguous()
+    assert tuple(w.codes.shape) == (w.E * w.N, w.K // 2)
+    assert w.sf.dtype == U8 and w.sf.is_contiguous()
+    assert w.sf.numel() >= w.E * sf_bytes(w.N, w.K)
+    assert w.gs.dtype == F32 and w.gs.is_contiguous() and w.gs.numel() >= w.E
+
+
+def _row_stride(x):
+    """Row stride of a 2-D tensor (a single row has none that matters)."""
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
+
+
+def linear_w4a16(x, w: "NVFP4Weights", out_dtype=BF16, out=None):
+    """out (M, N) = x W^T with bf16 x (M, K) used as it is (not quantized, unlike linear()) and W
+    one NVFP4 matrix (w.E == 1): for up to a few dozen rows.  out_dtype bf16 or float32; N is
+    any, K % 64 == 0.  One launch, no workspace."""
+    assert x.dtype == BF16 and x.dim() == 2 and x.stride(1) == 1 and w.E == 1
+    assert out_dtype in (BF16, F32)
+    M, K = x.shape
+    assert K == w.K
+    _check_weights(w, x.device)
+    if out is None:
+        out = torch.empty(M, w.N, dtype=out_dtype, device=x.device)
+    _check_on(x.device, out=out)
+    assert out.dtype == out_dtype and tuple(out.shape) == (M, w.N) and out.is_contiguous()
+    with _on_device(x):
+        call("nvfp4_linear_w4a16", _p(x), M, K, _row_stride(x), _p(w.codes), _p(w.sf), _p(w.gs),
+             w.N, _p(out), 0 if out_dtype == F32 else 1, _stream())
+    return out
+
+
+def moe_ffn_w4a16_workspace_bytes(T, H, I, E, k):
+    return int(lib().moe_ffn_w4a16_workspace_size(T, H, I, E, k))
+
+
+def moe_ffn_w4a16(x, logits, k, w1: NVFP4Weights, w2: NVFP4Weights, ids=None, weights=None,
+                  out=None, ws=None, status=None):
+    """The expert FFN of a small batch with unquantized activations: bf16 x (T, H) -> bf16
+    (T, H).  Routing from float32 logits (T, E), or logits=None with ids (T, k) int32 (< 0:
+    dropped slot) and weights (T, k) float32.  w1 from quantize_w1, w2 from quantize_weights; T * k
+    at most 4096 (moe_ffn_forward takes larger batches)."""
+    assert x.dtype == BF16 and x.dim() == 2 and x.is_contiguous()
+    T, H = x.shape
+    E, I = w1.E, w1.N // 2
+    assert w2.E == E and w1.K == H and w2.N == H and w2.K == I
+    dev = x.device
+    _check_weights(w1, dev)
+    _check_weights(w2, dev)
+    _check_on(dev, logits=logits, ids=ids, weights=weights, out=out, ws=ws, status=status)
+    if logits is not None:
+        assert ids is None and weights is None
+        assert logits.dtype == F32 and tuple(logits.shape) == (T, E) and logits.is_contiguous()
+    else:
+        assert ids.dtype == I32 and tuple(ids.shape) == (T, k) and ids.is_contiguous()
+        assert weights.dtype == F32 and tuple(weights.shape) == (T, k) and weights.is_contiguous()
+    if out is None:
+        out = torch.empty(T, H, dtype=BF16, device=dev)
+    assert out.dtype == BF16 and tuple(out.shape) == (T, H) and out.is_contiguous()
+    with _on_device(x):
+        if ws is None:
+            ws = torch.empty(max(moe_ffn_w4a16_workspace_bytes(T, H, I, E, k), 256), dtype=U8,
+                             device=dev)
+        call("moe_ffn_w4a16", _p(x), _p(logits), _p(ids), _p(weights), T, H, I, E, k, _p(w1.codes),
+             _p(w1.sf), _p(w1.gs), _p(w2.codes), _p(w2.sf), _p(w2.gs), _p(out), _p(ws), ws.numel(),
+             _p(status), _stream())
     return out
 
 

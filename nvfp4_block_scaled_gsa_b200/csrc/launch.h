@@ -22,6 +22,11 @@ nvfp4_status_t permute_launch(const float* logits, int T, int E, int k, int reno
                               int32_t* topk_ids, float* topk_w, int32_t* offs, int32_t* dst_row,
                               int32_t* row_slot, float* row_w, int64_t R_max, int32_t* hist_ws,
                               int32_t* dev_status, cudaStream_t s);
+// Top-k (with logits) and the slots of a small batch bucketed by expert: plan[i] = {expert, first
+// position in order, count, 0} for the *n_plan busy experts, ascending.
+nvfp4_status_t slot_plan_launch(const float* logits, int T, int E, int k, int32_t* ids, float* w,
+                                int4* plan, int32_t* n_plan, int32_t* order, int32_t* dev_status,
+                                cudaStream_t s);
 size_t permute_workspace_bytes(int T, int E, int k);
 
 nvfp4_status_t gemm_dense(const uint8_t* a, const uint8_t* sfa, const float* gs_a,

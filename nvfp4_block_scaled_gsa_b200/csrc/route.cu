@@ -254,7 +254,74 @@ __global__ void __launch_bounds__(1024) permute_kernel(
   }
 }
 
+// The plan of a small batch: slots bucketed by expert without padding rows.  One CTA, all of it
+// in shared memory: top-k (with logits), counts, an exclusive scan, and the slots in place.  The
+// order of an expert's slots is whatever the atomics give; a slot's result does not depend on it
+// (each is a column of its own).
+__global__ void __launch_bounds__(1024) slot_plan_kernel(
+    const float* __restrict__ logits, int T, int E, int k, int32_t* ids, float* w,
+    int4* __restrict__ plan, int32_t* __restrict__ n_plan, int32_t* __restrict__ order,
+    int32_t* __restrict__ dev_status) {
+  __shared__ int cnt[kMaxE];
+  __shared__ int cursor[kMaxE];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid < kMaxE) cnt[tid] = 0;
+  if (logits != nullptr)
+    for (int t = warp; t < T; t += 32) topk_token(logits, t, E, k, 1, lane, ids, w);
+  __syncthreads();  // also: this CTA's ids are visible to all its threads
+  const int S = T * k;
+  bool bad = false;
+  for (int s = tid; s < S; s += blockDim.x) {
+    const int e = ids[s];
+    if (e >= E) bad = true;
+    else if (e >= 0) atomicAdd(&cnt[e], 1);
+  }
+  if (bad) report(dev_status, NVFP4_DEVERR_BAD_INDEX);
+  __syncthreads();
+  if (warp == 0) {  // lane l: experts 8l..8l+7
+    int c[kPerLane], sum = 0, busy = 0;
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) {
+      c[i] = cnt[lane * kPerLane + i];
+      sum += c[i];
+      busy += c[i] > 0;
+    }
+    int run = sum, at = busy;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, run, o);
+      const int b = __shfl_up_sync(0xffffffffu, at, o);
+      if (lane >= o) {
+        run += v;
+        at += b;
+      }
+    }
+    if (lane == 31) *n_plan = at;
+    run -= sum;
+    at -= busy;
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) {
+      cursor[lane * kPerLane + i] = run;
+      if (c[i] > 0) plan[at++] = make_int4(lane * kPerLane + i, run, c[i], 0);
+      run += c[i];
+    }
+  }
+  __syncthreads();
+  for (int s = tid; s < S; s += blockDim.x) {
+    const int e = ids[s];
+    if (e >= 0 && e < E) order[atomicAdd(&cursor[e], 1)] = s;
+  }
+}
+
 }  // namespace
+
+nvfp4_status_t slot_plan_launch(const float* logits, int T, int E, int k, int32_t* ids, float* w,
+                                int4* plan, int32_t* n_plan, int32_t* order, int32_t* dev_status,
+                                cudaStream_t s) {
+  slot_plan_kernel<<<1, 1024, 0, s>>>(logits, T, E, k, ids, w, plan, n_plan, order, dev_status);
+  return check_launch("slot_plan_kernel");
+}
 
 int permute_chunks(int T, int k) {
   const int64_t S = (int64_t)T * k;
