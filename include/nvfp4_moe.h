@@ -502,7 +502,7 @@ NVFP4_API nvfp4_status_t moe_ffn_forward_ex(const void* x_bf16, const float* log
 
 /* ---------------------------------------------------------------------------------------------
  * nvfp4_linear_w4a16 — out = x W^T with NVFP4 weights and the activations as they are, for few
- * rows: one launch that reads the weights once.
+ * rows: the weights are read once.
  *
  * nvfp4_linear quantizes its activations to 4 bits, which costs accuracy and, for a handful of
  * rows, launches that take longer than the weights' transfer.  This call multiplies the same
@@ -517,11 +517,15 @@ NVFP4_API nvfp4_status_t moe_ffn_forward_ex(const void* x_bf16, const float* log
  *   Infinities and NaNs of x reach the outputs of their own row only.  Results do not depend on
  *   M or on the other rows' values except through the summation order, which M, N, K and the
  *   device's SM count fix (the result is reproducible).
+ *   ws        device scratch of nvfp4_linear_w4a16_workspace_size(M, K) bytes (x in the order the
+ *             product reads it, one word per row)
  *   Constraints: K % 64 == 0, any N >= 1, M <= 2,097,120.
  * ------------------------------------------------------------------------------------------- */
+NVFP4_API size_t nvfp4_linear_w4a16_workspace_size(int64_t M, int K);
 NVFP4_API nvfp4_status_t nvfp4_linear_w4a16(const void* x, int64_t M, int K, int64_t ld,
                                             const uint8_t* w, const uint8_t* sfw,
                                             const float* gs_w, int N, void* out, int out_dtype,
+                                            void* ws, size_t ws_bytes, int32_t* dev_status,
                                             nvfp4_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------------

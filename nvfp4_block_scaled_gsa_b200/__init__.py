@@ -17,6 +17,7 @@ from .api import (  # noqa: F401
     l2_scatter_add,
     linear,
     linear_w4a16,
+    linear_w4a16_workspace_bytes,
     linear_workspace_bytes,
     moe_ffn_forward,
     moe_ffn_w4a16,

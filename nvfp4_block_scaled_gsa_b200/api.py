@@ -356,25 +356,33 @@ def moe_ffn_forward_ex(x, logits, k, w1: NVFP4Weights, w2: NVFP4Weights, gs_h, d
     return out
 
 
-def _on_device(t):
-    """Context that makes t's device current (a no-op when it is)."""
-    assert t.is_cuda
-    return torch.cuda.device(t.device)
+def _call_on(dev, name, *args):
+    """call(name, *args, stream) with dev current, on its current stream."""
+    if dev.index == torch.cuda.current_device():
+        call(name, *args, torch._C._cuda_getCurrentRawStream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            call(name, *args, torch._C._cuda_getCurrentRawStream(dev.index))
 
 
-def _check_on(dev, **tensors):
-    for name, t in tensors.items():
-        assert t is None or t.device == dev, f"{name} is not on {dev}"
+def _same_device(dev, *tensors):
+    assert dev.type == "cuda", "CUDA tensors only"
+    for t in tensors:
+        assert t is None or t.device == dev, f"all tensors must be on {dev}"
 
 
 def _check_weights(w: "NVFP4Weights", dev):
     """The buffers of w as the kernels index them."""
-    _check_on(dev, codes=w.codes, sf=w.sf, gs=w.gs)
-    assert w.codes.dtype == U8 and w.codes.is_contiguous()
-    assert tuple(w.codes.shape) == (w.E * w.N, w.K // 2)
-    assert w.sf.dtype == U8 and w.sf.is_contiguous()
-    assert w.sf.numel() >= w.E * sf_bytes(w.N, w.K)
-    assert w.gs.dtype == F32 and w.gs.is_contiguous() and w.gs.numel() >= w.E
+    codes, sf, gs = w.codes, w.sf, w.gs
+    _same_device(dev, codes, sf, gs)
+    assert codes.dtype == U8 and codes.is_contiguous() and codes.shape == (w.E * w.N, w.K // 2)
+    assert sf.dtype == U8 and sf.is_contiguous() and sf.numel() >= w.E * sf_bytes(w.N, w.K)
+    assert gs.dtype == F32 and gs.is_contiguous() and gs.numel() >= w.E
+
+
+def _bytes(ws):
+    assert ws.is_contiguous()
+    return ws.numel() * ws.element_size()
 
 
 def _row_stride(x):
@@ -382,22 +390,28 @@ def _row_stride(x):
     return x.stride(0) if x.shape[0] > 1 else x.shape[1]
 
 
-def linear_w4a16(x, w: "NVFP4Weights", out_dtype=BF16, out=None):
+def linear_w4a16_workspace_bytes(M, K):
+    return int(lib().nvfp4_linear_w4a16_workspace_size(M, K))
+
+
+def linear_w4a16(x, w: "NVFP4Weights", out_dtype=BF16, out=None, ws=None, status=None):
     """out (M, N) = x W^T with bf16 x (M, K) used as it is (not quantized, unlike linear()) and W
-    one NVFP4 matrix (w.E == 1): for up to a few dozen rows.  out_dtype bf16 or float32; N is
-    any, K % 64 == 0.  One launch, no workspace."""
+    one NVFP4 matrix (w.E == 1): for up to a few dozen rows.  out_dtype bf16 or float32; any N,
+    K % 64 == 0."""
     assert x.dtype == BF16 and x.dim() == 2 and x.stride(1) == 1 and w.E == 1
     assert out_dtype in (BF16, F32)
     M, K = x.shape
+    dev = x.device
     assert K == w.K
-    _check_weights(w, x.device)
+    _check_weights(w, dev)
+    _same_device(dev, out, ws, status)
     if out is None:
-        out = torch.empty(M, w.N, dtype=out_dtype, device=x.device)
-    _check_on(x.device, out=out)
-    assert out.dtype == out_dtype and tuple(out.shape) == (M, w.N) and out.is_contiguous()
-    with _on_device(x):
-        call("nvfp4_linear_w4a16", _p(x), M, K, _row_stride(x), _p(w.codes), _p(w.sf), _p(w.gs),
-             w.N, _p(out), 0 if out_dtype == F32 else 1, _stream())
+        out = torch.empty(M, w.N, dtype=out_dtype, device=dev)
+    assert out.dtype == out_dtype and out.shape == (M, w.N) and out.is_contiguous()
+    if ws is None:
+        ws = torch.empty(linear_w4a16_workspace_bytes(M, K), dtype=U8, device=dev)
+    _call_on(dev, "nvfp4_linear_w4a16", _p(x), M, K, _row_stride(x), _p(w.codes), _p(w.sf),
+             _p(w.gs), w.N, _p(out), 0 if out_dtype == F32 else 1, _p(ws), _bytes(ws), _p(status))
     return out
 
 
@@ -418,23 +432,22 @@ def moe_ffn_w4a16(x, logits, k, w1: NVFP4Weights, w2: NVFP4Weights, ids=None, we
     dev = x.device
     _check_weights(w1, dev)
     _check_weights(w2, dev)
-    _check_on(dev, logits=logits, ids=ids, weights=weights, out=out, ws=ws, status=status)
+    _same_device(dev, logits, ids, weights, out, ws, status)
     if logits is not None:
         assert ids is None and weights is None
-        assert logits.dtype == F32 and tuple(logits.shape) == (T, E) and logits.is_contiguous()
+        assert logits.dtype == F32 and logits.shape == (T, E) and logits.is_contiguous()
     else:
-        assert ids.dtype == I32 and tuple(ids.shape) == (T, k) and ids.is_contiguous()
-        assert weights.dtype == F32 and tuple(weights.shape) == (T, k) and weights.is_contiguous()
+        assert ids.dtype == I32 and ids.shape == (T, k) and ids.is_contiguous()
+        assert weights.dtype == F32 and weights.shape == (T, k) and weights.is_contiguous()
     if out is None:
         out = torch.empty(T, H, dtype=BF16, device=dev)
-    assert out.dtype == BF16 and tuple(out.shape) == (T, H) and out.is_contiguous()
-    with _on_device(x):
-        if ws is None:
-            ws = torch.empty(max(moe_ffn_w4a16_workspace_bytes(T, H, I, E, k), 256), dtype=U8,
-                             device=dev)
-        call("moe_ffn_w4a16", _p(x), _p(logits), _p(ids), _p(weights), T, H, I, E, k, _p(w1.codes),
-             _p(w1.sf), _p(w1.gs), _p(w2.codes), _p(w2.sf), _p(w2.gs), _p(out), _p(ws), ws.numel(),
-             _p(status), _stream())
+    assert out.dtype == BF16 and out.shape == (T, H) and out.is_contiguous()
+    if ws is None:
+        ws = torch.empty(max(moe_ffn_w4a16_workspace_bytes(T, H, I, E, k), 256), dtype=U8,
+                         device=dev)
+    _call_on(dev, "moe_ffn_w4a16", _p(x), _p(logits), _p(ids), _p(weights), T, H, I, E, k,
+             _p(w1.codes), _p(w1.sf), _p(w1.gs), _p(w2.codes), _p(w2.sf), _p(w2.gs), _p(out),
+             _p(ws), _bytes(ws), _p(status))
     return out
 
 

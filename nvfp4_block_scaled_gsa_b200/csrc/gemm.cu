@@ -1030,6 +1030,10 @@ int dense_k_splits(int64_t M, int N, int K, int sms, int64_t part_floats) {
 
 int device_sms() { return num_sms(); }
 
+bool byte_tensor_map(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows) {
+  return make_map(m, base, row_bytes, rows);
+}
+
 // FP32 partial products of a dense C = A B^T over ks K ranges, plane r = range r, M rows of N
 // floats each, for a consumer that finishes the sum itself.  ks comes from dense_k_splits (so
 // ks <= K/256 and the rows stay below the pair-tile threshold).

@@ -2,6 +2,7 @@
 // the C ABI).  Each validates nothing: the extern "C" entry points check their arguments first.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -22,11 +23,6 @@ nvfp4_status_t permute_launch(const float* logits, int T, int E, int k, int reno
                               int32_t* topk_ids, float* topk_w, int32_t* offs, int32_t* dst_row,
                               int32_t* row_slot, float* row_w, int64_t R_max, int32_t* hist_ws,
                               int32_t* dev_status, cudaStream_t s);
-// Top-k (with logits) and the slots of a small batch bucketed by expert: plan[i] = {expert, first
-// position in order, count, 0} for the *n_plan busy experts, ascending.
-nvfp4_status_t slot_plan_launch(const float* logits, int T, int E, int k, int32_t* ids, float* w,
-                                int4* plan, int32_t* n_plan, int32_t* order, int32_t* dev_status,
-                                cudaStream_t s);
 size_t permute_workspace_bytes(int T, int E, int k);
 
 nvfp4_status_t gemm_dense(const uint8_t* a, const uint8_t* sfa, const float* gs_a,
@@ -35,6 +31,8 @@ nvfp4_status_t gemm_dense(const uint8_t* a, const uint8_t* sfa, const float* gs_
                           cudaStream_t s);
 int dense_k_splits(int64_t M, int N, int K, int sms, int64_t part_floats);
 int device_sms();
+// 2D byte tensor [rows][row_bytes] in boxes of 128 rows x 128 bytes, 128-byte swizzle.
+bool byte_tensor_map(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows);
 nvfp4_status_t gemm_dense_parts(const uint8_t* a, const uint8_t* sfa, const float* gs_a,
                                 const uint8_t* b, const uint8_t* sfb, const float* gs_b,
                                 int64_t M, int N, int K, int ks, float* part, int32_t* status,

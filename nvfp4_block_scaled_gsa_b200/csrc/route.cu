@@ -10,75 +10,10 @@
 #include <float.h>
 
 #include "common.cuh"
+#include "topk.cuh"
 
 namespace nvfp4 {
 namespace {
-
-constexpr int kMaxE = 256;
-constexpr int kMaxK = 32;
-constexpr int kPerLane = kMaxE / 32;
-
-// Top-k of token t by one warp.  Lane l holds experts l, l+32, ..., and lane j < k ends up
-// holding the j-th selected expert.
-__device__ __forceinline__ void topk_token(const float* __restrict__ logits, int t, int E, int k,
-                                           int renorm, int lane, int32_t* ids, float* w) {
-  float v[kPerLane];
-  float m = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < kPerLane; ++i) {
-    const int e = lane + 32 * i;
-    v[i] = e < E ? __ldg(logits + (int64_t)t * E + e) : -INFINITY;
-    if (e < E) m = fmaxf(m, v[i]);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-
-  uint32_t taken = 0;
-  int my_id = -1;
-  float my_v = -INFINITY;
-  for (int j = 0; j < k; ++j) {
-    float bv = -INFINITY;
-    int be = INT_MAX;
-#pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
-      const int e = lane + 32 * i;
-      if (e < E && !((taken >> i) & 1u) && (v[i] > bv || (v[i] == bv && e < be))) {
-        bv = v[i];
-        be = e;
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
-      const int oe = __shfl_xor_sync(0xffffffffu, be, o);
-      if (ov > bv || (ov == bv && oe < be)) {
-        bv = ov;
-        be = oe;
-      }
-    }
-    if (be != INT_MAX && (be & 31) == lane) taken |= 1u << (be >> 5);
-    if (lane == j) {
-      my_id = be;
-      my_v = bv;
-    }
-  }
-  const bool live = lane < k && my_id != INT_MAX && my_v > -INFINITY && m > -INFINITY;
-  const float ex = live ? expf(my_v - m) : 0.0f;
-  float denom = 0.0f;
-  if (renorm) {
-    denom = ex;
-  } else {
-#pragma unroll
-    for (int i = 0; i < kPerLane; ++i)
-      if (lane + 32 * i < E && v[i] > -INFINITY && m > -INFINITY) denom += expf(v[i] - m);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) denom += __shfl_xor_sync(0xffffffffu, denom, o);
-  if (lane < k) {
-    ids[(int64_t)t * k + lane] = live ? my_id : -1;
-    w[(int64_t)t * k + lane] = live ? ex / denom : 0.0f;
-  }
-}
 
 // One warp per token.
 __global__ void __launch_bounds__(256) topk_kernel(const float* __restrict__ logits, int T, int E,
@@ -254,74 +189,7 @@ __global__ void __launch_bounds__(1024) permute_kernel(
   }
 }
 
-// The plan of a small batch: slots bucketed by expert without padding rows.  One CTA, all of it
-// in shared memory: top-k (with logits), counts, an exclusive scan, and the slots in place.  The
-// order of an expert's slots is whatever the atomics give; a slot's result does not depend on it
-// (each is a column of its own).
-__global__ void __launch_bounds__(1024) slot_plan_kernel(
-    const float* __restrict__ logits, int T, int E, int k, int32_t* ids, float* w,
-    int4* __restrict__ plan, int32_t* __restrict__ n_plan, int32_t* __restrict__ order,
-    int32_t* __restrict__ dev_status) {
-  __shared__ int cnt[kMaxE];
-  __shared__ int cursor[kMaxE];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (tid < kMaxE) cnt[tid] = 0;
-  if (logits != nullptr)
-    for (int t = warp; t < T; t += 32) topk_token(logits, t, E, k, 1, lane, ids, w);
-  __syncthreads();  // also: this CTA's ids are visible to all its threads
-  const int S = T * k;
-  bool bad = false;
-  for (int s = tid; s < S; s += blockDim.x) {
-    const int e = ids[s];
-    if (e >= E) bad = true;
-    else if (e >= 0) atomicAdd(&cnt[e], 1);
-  }
-  if (bad) report(dev_status, NVFP4_DEVERR_BAD_INDEX);
-  __syncthreads();
-  if (warp == 0) {  // lane l: experts 8l..8l+7
-    int c[kPerLane], sum = 0, busy = 0;
-#pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
-      c[i] = cnt[lane * kPerLane + i];
-      sum += c[i];
-      busy += c[i] > 0;
-    }
-    int run = sum, at = busy;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, run, o);
-      const int b = __shfl_up_sync(0xffffffffu, at, o);
-      if (lane >= o) {
-        run += v;
-        at += b;
-      }
-    }
-    if (lane == 31) *n_plan = at;
-    run -= sum;
-    at -= busy;
-#pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
-      cursor[lane * kPerLane + i] = run;
-      if (c[i] > 0) plan[at++] = make_int4(lane * kPerLane + i, run, c[i], 0);
-      run += c[i];
-    }
-  }
-  __syncthreads();
-  for (int s = tid; s < S; s += blockDim.x) {
-    const int e = ids[s];
-    if (e >= 0 && e < E) order[atomicAdd(&cursor[e], 1)] = s;
-  }
-}
-
 }  // namespace
-
-nvfp4_status_t slot_plan_launch(const float* logits, int T, int E, int k, int32_t* ids, float* w,
-                                int4* plan, int32_t* n_plan, int32_t* order, int32_t* dev_status,
-                                cudaStream_t s) {
-  slot_plan_kernel<<<1, 1024, 0, s>>>(logits, T, E, k, ids, w, plan, n_plan, order, dev_status);
-  return check_launch("slot_plan_kernel");
-}
 
 int permute_chunks(int T, int k) {
   const int64_t S = (int64_t)T * k;
