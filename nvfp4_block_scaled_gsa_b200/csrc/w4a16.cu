@@ -21,13 +21,11 @@
 //
 // Layout.  A warp owns 32 rows of a 128-row block, rows 8*rg + g + 32*i (g = lane/4, i < 4), and
 // per step 256 elements of K, lane q = lane%4 the 64 elements from 64*q: 32 bytes of codes per
-// row (two warps share them) and one 16-byte line of a scale atom, which holds the scales of
-// exactly those 4 rows and 64 elements.  The order of K inside a step is free as long as both operands agree, so a lane's
+// row and one 16-byte line of a scale atom, which holds the scales of exactly those 4 rows and
+// 64 elements.  The order of K inside a step is free as long as both operands agree, so a lane's
 // own 4 weights of a row are the 4 K positions the MMA wants from it, and the converted
 // activations are stored in that order.
 #include <cuda_fp16.h>
-
-#include <type_traits>
 
 #include "common.cuh"
 #include "launch.h"
@@ -37,7 +35,7 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kRowWarps = 4;               // 4 x 32 rows = one 128-row scale atom
-constexpr int kKWarps = 2;                 // warps that share 32 rows, each over half of every step
+constexpr int kKWarps = 2;                 // warps that share a row group, taking steps in turn
 constexpr int kConsumers = kRowWarps * kKWarps;
 constexpr int kThreads = 32 * (kConsumers + 1);  // and one warp that issues the copies
 constexpr int kStepK = 256;                // elements of K per step
@@ -57,9 +55,10 @@ struct Cfg {
   // two CTAs per SM with up to 16 tokens (so that one's start and end overlap the other's
   // stream), one with 32, whose accumulators need the registers
   static constexpr int CTAS = NT == 4 ? 1 : 2;
-  static constexpr int STAGES = NT == 1 ? 4 : NT == 2 ? 3 : 5;
+  static constexpr int STAGES = NT == 4 ? 6 : 4;
   static constexpr int SMEM = STAGES * STAGE + 1024;
   static_assert(kKWarps * TOK * kRedStride * 4 <= STAGES * STAGE, "partial sums reuse the stages");
+  static_assert(STAGES % kKWarps == 0, "a stage is always the same K warps', or one could wait two phases ahead");
   static_assert(CTAS * (SMEM + 3072) <= 227 * 1024, "shared memory of an SM");
 };
 
@@ -350,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::CTAS)
     abort_flag = 0;
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(smem_u32(&bar_full[i]), 1);
-      mbar_init(smem_u32(&bar_empty[i]), kConsumers);
+      mbar_init(smem_u32(&bar_empty[i]), kRowWarps);
     }
     fence_mbar_init();
   }
@@ -459,83 +458,85 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::CTAS)
         s_row[tid] = r;
         s_exp[tid] = ld_after(A.exps + x_row(r));
       }
-      // Row warps rg, each with two K warps that take the first or the second half of every
-      // lane's 64 elements, so that a stage is held no longer than its products take.
       const int rg = warp % kRowWarps, wk = warp / kRowWarps;
-      // this lane's 16-byte piece of a row's 128 bytes (128-byte swizzle: the piece index is xored
-      // with the row's index modulo 8, which is g for all of the lane's rows)
-      const int code_off = (8 * rg + g) * 128 + ((2 * q + wk) ^ g) * 16;
+      // this lane's two 16-byte pieces of a row's 128 bytes (128-byte swizzle: the piece index is
+      // xored with the row's index modulo 8, which is g for all of the lane's rows)
+      const int row_off = (8 * rg + g) * 128;
+      const int piece[2] = {((2 * q) ^ g) * 16, ((2 * q + 1) ^ g) * 16};
       const int scale_off = kWTile + q * 512 + (8 * rg + g) * 16;
-      // The sums of two steps start from zero and are added to the running sums in plain float32
-      // (the MMA truncates as it accumulates, and over a long K that would drift).
-      float tmp[CH][2][NT][4];
-      auto step = [&](int i, auto fresh) {
+      for (int i = wk; i < n_st; i += kKWarps) {
         const uint32_t it = it0 + i, s = it % STAGES;
         const bool mine = mbar_wait_bounded(smem_u32(&bar_full[s]), (it / STAGES) & 1u, &abort_flag);
-        if (!__all_sync(0xffffffffu, mine)) return false;
+        if (!__all_sync(0xffffffffu, mine)) break;
         const uint8_t* st = smem + s * C::STAGE;
         const uint8_t* xb[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-          xb[n] = (n * 8 + g < ntok ? st + kWTile + kSTile + (n * 8 + g) * kXRow : zeros) +
-                  wk * (kStepX / 2) + q * 16;
-        uint32_t sc[4], w[4][4];
+          xb[n] = (n * 8 + g < ntok ? st + kWTile + kSTile + (n * 8 + g) * kXRow : zeros) + q * 16;
+        // One step: 8 words of 8 codes per row.  The sums of a step start from zero and are added
+        // to the running sums in plain float32 (the MMA truncates as it accumulates, and over a
+        // long K that would drift).
+        uint32_t sc[4][2];
         {
           uint4 sv = lds16(st + scale_off);
           // past K the codes are zeros, but the scale bytes are whatever was there
           if ((st0 + i) * kStepK + q * 64 >= A.K) sv = make_uint4(0u, 0u, 0u, 0u);
           const uint32_t sw[4] = {sv.x, sv.y, sv.z, sv.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) sc[j] = decode_scales(sw[j] >> (16 * wk));
+          for (int j = 0; j < 4; ++j) {
+            sc[j][0] = decode_scales(sw[j] & 0xFFFFu);
+            sc[j][1] = decode_scales(sw[j] >> 16);
+          }
         }
+        float tmp[CH][2][NT][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint4 v = lds16(st + code_off + j * (32 * 128));
-          w[j][0] = v.x;
-          w[j][1] = v.y;
-          w[j][2] = v.z;
-          w[j][3] = v.w;
-        }
+        for (int half = 0; half < 2; ++half) {
+          uint32_t w[4][4];
 #pragma unroll
-        for (int wd = 0; wd < 4; ++wd) {
-          uint4 b[NT];
+          for (int j = 0; j < 4; ++j) {
+            const uint4 v = lds16(st + row_off + j * (32 * 128) + piece[half]);
+            w[j][0] = v.x;
+            w[j][1] = v.y;
+            w[j][2] = v.z;
+            w[j][3] = v.w;
+          }
 #pragma unroll
-          for (int n = 0; n < NT; ++n) b[n] = lds16(xb[n] + wd * 64);
+          for (int wd = 0; wd < 4; ++wd) {
+            uint4 b[NT];
 #pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            uint32_t a[2][4];
+            for (int n = 0; n < NT; ++n) b[n] = lds16(xb[n] + half * 256 + wd * 64);
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              decode8(w[2 * p + r][wd], a[r]);
-              // the scale of 16-element group 2 * wk + wd / 2, in both halves
-              const uint32_t sv = __byte_perm(sc[2 * p + r], 0u, (wd & 2) ? 0x3232u : 0x1010u);
+            for (int p = 0; p < 2; ++p) {
+              uint32_t a[2][4];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) a[r][j] = mul_f16x2(a[r][j], sv);
-            }
+              for (int r = 0; r < 2; ++r) {
+                decode8(w[2 * p + r][wd], a[r]);
+                // the scale of 16-element group 2 * half + wd / 2, in both halves
+                const uint32_t sv =
+                    __byte_perm(sc[2 * p + r][half], 0u, (wd & 2) ? 0x3232u : 0x1010u);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              auto& t0 = tmp[0][p][n];
-              auto& t1 = tmp[CH - 1][p][n];
-              if (decltype(fresh)::value && wd == 0) {
-                mma_f16_first(t0, a[0][0], a[1][0], a[0][1], a[1][1], b[n].x, b[n].y);
-                if constexpr (CH == 2)
-                  mma_f16_first(t1, a[0][2], a[1][2], a[0][3], a[1][3], b[n].z, b[n].w);
-                else
+                for (int j = 0; j < 4; ++j) a[r][j] = mul_f16x2(a[r][j], sv);
+              }
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                auto& t0 = tmp[0][p][n];
+                auto& t1 = tmp[CH - 1][p][n];
+                if (half == 0 && wd == 0) {
+                  mma_f16_first(t0, a[0][0], a[1][0], a[0][1], a[1][1], b[n].x, b[n].y);
+                  if constexpr (CH == 2)
+                    mma_f16_first(t1, a[0][2], a[1][2], a[0][3], a[1][3], b[n].z, b[n].w);
+                  else
+                    mma_f16(t1, a[0][2], a[1][2], a[0][3], a[1][3], b[n].z, b[n].w);
+                } else {
+                  mma_f16(t0, a[0][0], a[1][0], a[0][1], a[1][1], b[n].x, b[n].y);
                   mma_f16(t1, a[0][2], a[1][2], a[0][3], a[1][3], b[n].z, b[n].w);
-              } else {
-                mma_f16(t0, a[0][0], a[1][0], a[0][1], a[1][1], b[n].x, b[n].y);
-                mma_f16(t1, a[0][2], a[1][2], a[0][3], a[1][3], b[n].z, b[n].w);
+                }
               }
             }
           }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bar_empty[s]));
-        return true;
-      };
-      for (int i = 0; i < n_st; i += 2) {
-        if (!step(i, std::true_type{})) break;
-        if (i + 1 < n_st && !step(i + 1, std::false_type{})) break;
 #pragma unroll
         for (int p = 0; p < 2; ++p)
 #pragma unroll
@@ -669,13 +670,13 @@ __global__ void __launch_bounds__(256) combine_slots_kernel(const float* ys, con
 
 // ------------------------------------------------------------------------------ host side
 
-// CTAs along K for one output block: enough CTAs to give every SM two, while each keeps at least
-// two steps.
+// CTAs along K for one output block: enough CTAs for every SM, while each K warp keeps
+// at least one step.
 int pick_splits(int64_t blocks, int K, int most) {
   const int steps = (K + kStepK - 1) / kStepK;
   const int sms = device_sms();
   int s = 1;
-  while (s < most && blocks * s < 2 * sms && steps / (2 * s) >= 2) s *= 2;
+  while (s < most && blocks * s < sms && steps / (2 * s) >= kKWarps) s *= 2;
   return s;
 }
 
