@@ -514,14 +514,13 @@ NVFP4_API nvfp4_status_t moe_ffn_forward_ex(const void* x_bf16, const float* log
  *   w, sfw    NVFP4 [N][K] (codes [N][K/2], tiled scales), gs_w device float[1]
  *   out       [M][N], out_dtype 0 = float32, 1 = bf16:
  *             out[m][n] = sum_k x[m][k] * E2M1(w[n][k]) * E4M3(sfw[n][k/16]) / gs_w
- *   Infinities and NaNs of x reach the outputs of their own row only.  Results do not depend on
- *   M or on the other rows' values except through the summation order, which M, N, K and the
- *   device's SM count fix (the result is reproducible).
- *   ws        device scratch of nvfp4_linear_w4a16_workspace_size(M, K) bytes (x in the order the
- *             product reads it, one word per row)
+ *   Infinities and NaNs of x reach the outputs of their own row only.  The summation order is fixed
+ *   by M, N and K (the result is reproducible).
+ *   ws        device scratch of nvfp4_linear_w4a16_workspace_size(M, N, K) bytes (x in the order the
+ *             product reads it, one word per row); 0 = none needed (a few rows), ws may be NULL
  *   Constraints: K % 64 == 0, any N >= 1, M <= 2,097,120.
  * ------------------------------------------------------------------------------------------- */
-NVFP4_API size_t nvfp4_linear_w4a16_workspace_size(int64_t M, int K);
+NVFP4_API size_t nvfp4_linear_w4a16_workspace_size(int64_t M, int N, int K);
 NVFP4_API nvfp4_status_t nvfp4_linear_w4a16(const void* x, int64_t M, int K, int64_t ld,
                                             const uint8_t* w, const uint8_t* sfw,
                                             const float* gs_w, int N, void* out, int out_dtype,

@@ -77,7 +77,7 @@ SIGNATURES = {
     "moe_ffn_forward_ex": (c_int, [c_void, c_void, c_int, c_int, c_int, c_int, c_int, c_void,
                                    c_void, c_void, c_void, c_void, c_void, c_void, c_int, c_void,
                                    c_void, c_void, c_size, c_void, c_void]),
-    "nvfp4_linear_w4a16_workspace_size": (c_size, [c_i64, c_int]),
+    "nvfp4_linear_w4a16_workspace_size": (c_size, [c_i64, c_int, c_int]),
     "nvfp4_linear_w4a16": (c_int, [c_void, c_i64, c_int, c_i64, c_void, c_void, c_void, c_int,
                                    c_void, c_int, c_void, c_size, c_void, c_void]),
     "moe_ffn_w4a16_workspace_size": (c_size, [c_int, c_int, c_int, c_int, c_int]),

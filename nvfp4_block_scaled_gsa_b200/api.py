@@ -381,6 +381,8 @@ def _check_weights(w: "NVFP4Weights", dev):
 
 
 def _bytes(ws):
+    if ws is None:
+        return 0
     assert ws.is_contiguous()
     return ws.numel() * ws.element_size()
 
@@ -390,8 +392,8 @@ def _row_stride(x):
     return x.stride(0) if x.shape[0] > 1 else x.shape[1]
 
 
-def linear_w4a16_workspace_bytes(M, K):
-    return int(lib().nvfp4_linear_w4a16_workspace_size(M, K))
+def linear_w4a16_workspace_bytes(M, N, K):
+    return int(lib().nvfp4_linear_w4a16_workspace_size(M, N, K))
 
 
 def linear_w4a16(x, w: "NVFP4Weights", out_dtype=BF16, out=None, ws=None, status=None):
@@ -409,7 +411,9 @@ def linear_w4a16(x, w: "NVFP4Weights", out_dtype=BF16, out=None, ws=None, status
         out = torch.empty(M, w.N, dtype=out_dtype, device=dev)
     assert out.dtype == out_dtype and out.shape == (M, w.N) and out.is_contiguous()
     if ws is None:
-        ws = torch.empty(linear_w4a16_workspace_bytes(M, K), dtype=U8, device=dev)
+        need = linear_w4a16_workspace_bytes(M, w.N, K)
+        if need > 0:
+            ws = torch.empty(need, dtype=U8, device=dev)
     _call_on(dev, "nvfp4_linear_w4a16", _p(x), M, K, _row_stride(x), _p(w.codes), _p(w.sf),
              _p(w.gs), w.N, _p(out), 0 if out_dtype == F32 else 1, _p(ws), _bytes(ws), _p(status))
     return out

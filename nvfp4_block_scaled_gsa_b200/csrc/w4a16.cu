@@ -27,6 +27,8 @@
 // activations are stored in that order.
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "launch.h"
 #include "topk.cuh"
@@ -47,16 +49,21 @@ constexpr int kSTile = 4 * 512;            // its scale atoms
 // shared-memory phase (2 tokens x 4 quads of 16 bytes) touch every bank once.
 constexpr int kXRow = kStepX + 64;
 constexpr int kRedStride = 128 + 4;
+// XIN: activations that a CTA converts itself, in pieces of one token's step (two per warp, held in
+// registers between the two passes).  At 1 x 4096 x 7168 (4 pieces a CTA) 7.4 us against 8.4 us
+// with a converting kernel in front; with 28 pieces (1 x 65536 x 7168, 512 CTAs) 58 against 55.
+constexpr int kMaxPieces = 2 * kConsumers;
 
-template <int NT>
+template <int NT, bool XIN>
 struct Cfg {
   static constexpr int TOK = 8 * NT;  // token columns
-  static constexpr int STAGE = kWTile + kSTile + (TOK * kXRow + 1023) / 1024 * 1024;
+  static constexpr int STAGE = kWTile + kSTile + (XIN ? 0 : (TOK * kXRow + 1023) / 1024 * 1024);
   // two CTAs per SM with up to 16 tokens (so that one's start and end overlap the other's
   // stream), one with 32, whose accumulators need the registers
   static constexpr int CTAS = NT == 4 ? 1 : 2;
   static constexpr int STAGES = NT == 4 ? 6 : 4;
-  static constexpr int SMEM = STAGES * STAGE + 1024;
+  static constexpr int X_AT = STAGES * STAGE;  // XIN: the activations behind the stages
+  static constexpr int SMEM = X_AT + (XIN ? kMaxPieces * kXRow : 0) + 1024;
   static_assert(kKWarps * TOK * kRedStride * 4 <= STAGES * STAGE, "partial sums reuse the stages");
   static_assert(STAGES % kKWarps == 0, "a stage is always the same K warps', or one could wait two phases ahead");
   static_assert(CTAS * (SMEM + 3072) <= 227 * 1024, "shared memory of an SM");
@@ -68,8 +75,10 @@ struct Args {
   const uint8_t* sf;      // per expert round_up(N, 128) rows of tiled scales
   const float* gs;        // [E]
   int N, K;
-  const uint8_t* xf;      // converted activations, [rows][steps][kStepX bytes]
-  const int32_t* exps;    // [rows] power of two each row was multiplied by
+  const void* x;          // XIN: bf16 activations, rows of ld_bytes
+  int64_t ld_bytes;
+  const uint8_t* xf;      // else: converted ones, [rows][steps][kStepX bytes]
+  const int32_t* exps;    // and [rows] the power of two each row was multiplied by
   int M;                  // rows (DENSE)
   int k;                  // slots per token (FFN)
   const int4* plan;       // {expert, first, count, 0} per busy expert (FFN)
@@ -327,10 +336,17 @@ __global__ void __launch_bounds__(512) plan_kernel(
 
 // ------------------------------------------------------------------------- the product
 
-template <int NT, Mode MODE>
-__global__ void __launch_bounds__(kThreads, Cfg<NT>::CTAS)
+__device__ __forceinline__ void consumers_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory");
+}
+
+// XIN: the CTA converts the activations of its rows and its part of K itself, when they are few;
+// otherwise a kernel in front has converted them and they pass through the ring with the weights.
+template <int NT, Mode MODE, bool XIN>
+__global__ void __launch_bounds__(kThreads, Cfg<NT, XIN>::CTAS)
     w4a16_kernel(const __grid_constant__ CUtensorMap tm, const Args A) {
-  using C = Cfg<NT>;
+  static_assert(!XIN || MODE == DENSE, "the FFN's activations are converted in front");
+  using C = Cfg<NT, XIN>;
   constexpr int TOK = C::TOK, STAGES = C::STAGES;
   // Accumulators of one step: with one token tile each row pair has two, so that a warp's
   // consecutive MMAs do not wait for one another.
@@ -341,6 +357,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::CTAS)
   __shared__ volatile int abort_flag;
   __shared__ __align__(16) uint8_t zeros[kStepX];  // what columns without a token read
   __shared__ int s_row[TOK], s_exp[TOK];           // output row and power of two of each column
+  __shared__ uint32_t s_amax[TOK];                 // XIN
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, q = lane & 3;
   const int split = static_cast<int>(blockIdx.x) % A.splits;
@@ -375,6 +392,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::CTAS)
   const int atoms_k = A.K / 64;
   const int64_t blk_rows = (A.N + 127) / 128;
   const uint8_t* sf = A.sf + ((int64_t)e * blk_rows + rowblk) * atoms_k * 512;
+  const uint32_t gs_bits = __float_as_uint(__ldg(A.gs + e));  // a positive normal number
+  const int gs_exp = static_cast<int>(gs_bits >> 23) - 127;
+  const float gs_frac = __uint_as_float((gs_bits & 0x7FFFFFu) | 0x3F800000u);
   const int nsteps = (A.K + kStepK - 1) / kStepK;
   const int st0 = static_cast<int>((int64_t)nsteps * split / A.splits);
   const int n_st = static_cast<int>((int64_t)nsteps * (split + 1) / A.splits) - st0;
@@ -413,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::CTAS)
         if (lane == 0) {
           const int st = st0 + i, atoms = min(4, atoms_k - st * 4);
           const uint32_t bar = smem_u32(&bar_full[s]), d = smem_u32(smem + s * C::STAGE);
-          mbar_arrive_expect_tx(bar, kWTile + atoms * 512 + ntok * kStepX);
+          mbar_arrive_expect_tx(bar, kWTile + atoms * 512 + (XIN ? 0 : ntok * kStepX));
           tma_load_2d(d, &tm, bar, st * 128, static_cast<int>(wrow));
           bulk_load(d + kWTile, sf + (int64_t)st * 4 * 512, atoms * 512, bar);
         }
@@ -422,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::CTAS)
       const uint8_t* xr = nullptr;
       auto copy_x = [&](int i) {  // lane t: token t
         const uint32_t s = (it0 + i) % STAGES;
-        if (lane < ntok)
+        if (!XIN && lane < ntok)
           bulk_load(smem_u32(smem + s * C::STAGE + kWTile + kSTile) + lane * kXRow,
                     xr + (int64_t)(st0 + i) * kStepX, kStepX, smem_u32(&bar_full[s]));
       };
@@ -436,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::CTAS)
       // the activations come from the kernel before (and for the L1 and later token blocks this
       // has been waited for already)
       pdl_wait();
-      if (lane < ntok) xr = A.xf + (int64_t)x_row(out_row(lane)) * nsteps * kStepX;
+      if (!XIN && lane < ntok) xr = A.xf + (int64_t)x_row(out_row(lane)) * nsteps * kStepX;
       for (int i = 0; i < issued; ++i) copy_x(i);
       for (; issued < n_st && ok; ++issued) {
         ok = wait_empty(issued);
@@ -456,7 +476,40 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::CTAS)
         pdl_wait();
         const int r = out_row(tid);
         s_row[tid] = r;
-        s_exp[tid] = ld_after(A.exps + x_row(r));
+        if (!XIN) s_exp[tid] = ld_after(A.exps + x_row(r));
+      }
+      if constexpr (XIN) {
+        // pieces (token, step) warp and warp + kConsumers: lane l holds elements 8l .. 8l + 7
+        const int pieces = ntok * n_st;
+        X8<false> c[kMaxPieces / kConsumers];
+#pragma unroll
+        for (int j = 0; j < kMaxPieces / kConsumers; ++j) {
+          const int p = warp + j * kConsumers, k = (st0 + p % n_st) * kStepK + lane * 8;
+          if (p < pieces)
+            c[j].load(static_cast<const uint8_t*>(A.x) + (int64_t)(tb * TOK + p / n_st) * A.ld_bytes,
+                      k, k < A.K);
+        }
+        if (tid < TOK) s_amax[tid] = 0;
+        consumers_sync();
+#pragma unroll
+        for (int j = 0; j < kMaxPieces / kConsumers; ++j) {
+          const int p = warp + j * kConsumers;
+          if (p < pieces) {
+            const uint32_t m = __reduce_max_sync(0xffffffffu, c[j].amax());
+            if (lane == 0) atomicMax(&s_amax[p / n_st], m);
+          }
+        }
+        consumers_sync();
+        if (tid < TOK) s_exp[tid] = norm_exp(s_amax[tid]);
+#pragma unroll
+        for (int j = 0; j < kMaxPieces / kConsumers; ++j) {
+          const int p = warp + j * kConsumers;
+          if (p < pieces)
+            *reinterpret_cast<uint4*>(smem + C::X_AT + p * kXRow +
+                                      ((lane & 7) * 4 + (lane >> 3)) * 16) =
+                c[j].to_f16(pow2f(norm_exp(s_amax[p / n_st])));
+        }
+        consumers_sync();
       }
       const int rg = warp % kRowWarps, wk = warp / kRowWarps;
       // this lane's two 16-byte pieces of a row's 128 bytes (128-byte swizzle: the piece index is
@@ -472,7 +525,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::CTAS)
         const uint8_t* xb[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-          xb[n] = (n * 8 + g < ntok ? st + kWTile + kSTile + (n * 8 + g) * kXRow : zeros) + q * 16;
+          xb[n] = (n * 8 + g >= ntok ? zeros
+                   : XIN ? smem + C::X_AT + ((n * 8 + g) * n_st + i) * kXRow
+                         : st + kWTile + kSTile + (n * 8 + g) * kXRow) +
+                  q * 16;
         // One step: 8 words of 8 codes per row.  The sums of a step start from zero and are added
         // to the running sums in plain float32 (the MMA truncates as it accumulates, and over a
         // long K that would drift).
@@ -557,17 +613,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::CTAS)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < 2; ++c) {
+          const int t = n * 8 + 2 * q + c;
+          if (t >= ntok) continue;
+          // undo the row's power of two and the one in the global scale, in two exact steps (the
+          // rest of the global scale, in [1, 2), divides the total)
+          const int up = -s_exp[t] - gs_exp;  // within [-253, 240]
+          const float f0 = pow2f(up / 2), f1 = pow2f(up - up / 2);
 #pragma unroll
           for (int p = 0; p < 2; ++p)
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
-              red[(wk * TOK + n * 8 + 2 * q + c) * kRedStride + 8 * rg + g + 64 * p + 32 * r] =
-                  acc[p][n][2 * r + c];
+            for (int r = 0; r < 2; ++r) {
+              red[(wk * TOK + t) * kRedStride + 8 * rg + g + 64 * p + 32 * r] =
+                  acc[p][n][2 * r + c] * f0 * f1;
+            }
+        }
     }
     if (A.splits > 1) cluster_sync();
     else __syncthreads();
-    const float gs = __ldg(A.gs + e);
     auto total = [&](int row, int t) {
       const float* at = red + t * kRedStride + row;
       float v = 0.0f;
@@ -590,9 +653,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::CTAS)
 #pragma unroll
         for (int w = 0; w < kKWarps; ++w) v += at[w * TOK * kRedStride];
       }
-      // the row's power of two and the global scale, the one that shrinks the sum first
-      const int ne = s_exp[t];
-      return ne > 0 ? v * pow2f(-ne) / gs : v / gs * pow2f(-ne);
+      return v / gs_frac;
     };
     const int share = 128 / A.splits, r0 = share * split;
     if (!abort_flag) {
@@ -670,59 +731,80 @@ __global__ void __launch_bounds__(256) combine_slots_kernel(const float* ys, con
 
 // ------------------------------------------------------------------------------ host side
 
+// The SM count the K splits are sized for (on another device they are only less well chosen).
+constexpr int kSizingSms = 148;
+
 // CTAs along K for one output block: enough CTAs for every SM, while each K warp keeps
 // at least one step.
 int pick_splits(int64_t blocks, int K, int most) {
   const int steps = (K + kStepK - 1) / kStepK;
-  const int sms = device_sms();
   int s = 1;
-  while (s < most && blocks * s < sms && steps / (2 * s) >= kKWarps) s *= 2;
+  while (s < most && blocks * s < kSizingSms && steps / (2 * s) >= kKWarps) s *= 2;
   return s;
 }
 
 template <typename... P, typename... V>
 nvfp4_status_t launch_after(void (*fn)(P...), dim3 grid, int threads, size_t smem, int cluster,
-                            cudaStream_t s, const char* what, const V&... args) {
+                            bool early, cudaStream_t s, const char* what, const V&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = static_cast<unsigned>(cluster);
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  int n = 0;
+  if (early) {  // behind a kernel of this call: start while that one still runs
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = static_cast<unsigned>(cluster);
+    at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
+    ++n;
+  }
   cfg.attrs = at;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  cfg.numAttrs = static_cast<unsigned>(n);
   cudaLaunchKernelEx(&cfg, fn, P(args)...);
   return check_launch(what);
 }
 
-template <int NT, Mode MODE>
-nvfp4_status_t launch(const CUtensorMap& tm, const Args& a, dim3 grid, cudaStream_t s) {
-  auto* fn = w4a16_kernel<NT, MODE>;
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NT>::SMEM) !=
-      cudaSuccess)
-    return check_launch("w4a16_kernel attributes");
-  return launch_after(fn, grid, kThreads, Cfg<NT>::SMEM, a.splits, s, "w4a16_kernel", tm, a);
+template <int NT, Mode MODE, bool XIN>
+nvfp4_status_t launch(const CUtensorMap& tm, const Args& a, dim3 grid, bool early,
+                      cudaStream_t s) {
+  auto* fn = w4a16_kernel<NT, MODE, XIN>;
+  constexpr int smem = Cfg<NT, XIN>::SMEM;
+  // the attribute is set once per device (a call costs about as much as a launch)
+  static std::atomic<uint64_t> devices_set{0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!(devices_set.load(std::memory_order_acquire) & bit)) {
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+      return check_launch("w4a16_kernel attributes");
+    devices_set.fetch_or(bit, std::memory_order_release);
+  }
+  return launch_after(fn, grid, kThreads, smem, a.splits, early, s, "w4a16_kernel", tm, a);
 }
 
-// The product kernel over weights `codes` of `rows` rows, behind the kernel that prepares its
-// activations.
+bool weight_map(CUtensorMap* tm, const uint8_t* codes, int64_t rows, int K) {
+  if (byte_tensor_map(tm, codes, static_cast<uint64_t>(K / 2), static_cast<uint64_t>(rows)))
+    return true;
+  set_last_error("cuTensorMapEncodeTiled failed");
+  return false;
+}
+
+// The product kernel over weights `codes` of `rows` rows, behind the kernel of this call that
+// converts its activations.
 template <Mode MODE>
 nvfp4_status_t launch_nt(int nt, const uint8_t* codes, int64_t rows, const Args& a, dim3 grid,
                          cudaStream_t s) {
   CUtensorMap tm;
-  if (!byte_tensor_map(&tm, codes, static_cast<uint64_t>(a.K / 2), static_cast<uint64_t>(rows))) {
-    set_last_error("cuTensorMapEncodeTiled failed");
-    return NVFP4_ERR_CUDA;
-  }
+  if (!weight_map(&tm, codes, rows, a.K)) return NVFP4_ERR_CUDA;
   switch (nt) {
-    case 1: return launch<1, MODE>(tm, a, grid, s);
-    case 2: return launch<2, MODE>(tm, a, grid, s);
-    default: return launch<4, MODE>(tm, a, grid, s);
+    case 1: return launch<1, MODE, false>(tm, a, grid, true, s);
+    case 2: return launch<2, MODE, false>(tm, a, grid, true, s);
+    default: return launch<4, MODE, false>(tm, a, grid, true, s);
   }
 }
 
@@ -730,16 +812,28 @@ int64_t converted_bytes(int64_t rows, int K) {
   return rows * ((K + kStepK - 1) / kStepK) * kStepX;
 }
 
-// Byte offsets of the nvfp4_linear_w4a16 workspace regions (each 256-byte aligned).
-struct LinearW4Layout {
-  int64_t xf, exps, total;
+// How nvfp4_linear_w4a16 runs a shape, and the byte offsets of its workspace regions (256-byte
+// aligned; none when the CTAs convert the activations themselves).
+struct LinearW4Plan {
+  int nt, splits;
+  int64_t rowblks, tblks;
+  bool xin;
+  int64_t exps, total;
 };
 
-LinearW4Layout linear_w4_layout(int64_t M, int K) {
-  LinearW4Layout L{};
-  L.exps = round_up(converted_bytes(M, K), 256);
-  L.total = L.exps + round_up(M * 4, 256);
-  return L;
+LinearW4Plan linear_w4_plan(int64_t M, int N, int K) {
+  LinearW4Plan P{};
+  P.nt = M <= 8 ? 1 : M <= 16 ? 2 : 4;
+  P.rowblks = ((int64_t)N + 127) / 128;
+  P.tblks = (M + 8 * P.nt - 1) / (8 * P.nt);
+  P.splits = pick_splits(P.rowblks * P.tblks, K, kMaxSplits);
+  const int steps = (K + kStepK - 1) / kStepK;
+  P.xin = P.nt == 1 && M * ((steps + P.splits - 1) / P.splits) <= kMaxPieces;
+  if (!P.xin) {
+    P.exps = round_up(converted_bytes(M, K), 256);
+    P.total = P.exps + round_up(M * 4, 256);
+  }
+  return P;
 }
 
 // Byte offsets of the moe_ffn_w4a16 workspace regions (each 256-byte aligned).
@@ -776,9 +870,9 @@ FfnW4Layout ffn_w4_layout(int T, int H, int I, int E, int k) {
 
 using namespace nvfp4;
 
-extern "C" size_t nvfp4_linear_w4a16_workspace_size(int64_t M, int K) {
-  if (M < 0 || K <= 0) return 0;
-  return static_cast<size_t>(linear_w4_layout(M, K).total);
+extern "C" size_t nvfp4_linear_w4a16_workspace_size(int64_t M, int N, int K) {
+  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  return static_cast<size_t>(linear_w4_plan(M, N, K).total);
 }
 
 extern "C" nvfp4_status_t nvfp4_linear_w4a16(const void* x, int64_t M, int K, int64_t ld,
@@ -791,36 +885,41 @@ extern "C" nvfp4_status_t nvfp4_linear_w4a16(const void* x, int64_t M, int K, in
   if (K % 64 || ld % 8 || M > (int64_t)65535 * 32 || N > INT32_MAX - 127)
     return NVFP4_ERR_UNSUPPORTED_SHAPE;
   if (!w || !sfw || !gs_w) return NVFP4_ERR_INVALID_ARG;
-  if (M > 0 && (!x || !out || !ws)) return NVFP4_ERR_INVALID_ARG;
-  const LinearW4Layout L = linear_w4_layout(M, K);
-  if (M > 0 && (int64_t)ws_bytes < L.total) return NVFP4_ERR_WORKSPACE_TOO_SMALL;
+  if (M > 0 && (!x || !out)) return NVFP4_ERR_INVALID_ARG;
+  const LinearW4Plan P = linear_w4_plan(M, N, K);
+  if (M > 0 && P.total > 0 && (ws == nullptr || (int64_t)ws_bytes < P.total))
+    return NVFP4_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned16(x) || !aligned16(w) || !aligned16(sfw) || !aligned16(out) || !aligned16(ws) ||
       (reinterpret_cast<uintptr_t>(gs_w) & 3u) || (reinterpret_cast<uintptr_t>(dev_status) & 3u))
     return NVFP4_ERR_MISALIGNED;
   if (M == 0) return NVFP4_OK;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(ws);
-  convert_kernel<false><<<static_cast<unsigned>(M), 256, 0, s>>>(
-      x, ld * 2, K, base + L.xf, reinterpret_cast<int32_t*>(base + L.exps));
-  const nvfp4_status_t st = check_launch("convert_kernel");
-  if (st != NVFP4_OK) return st;
-  const int nt = M <= 8 ? 1 : M <= 16 ? 2 : 4;
-  const int64_t rowblks = (N + 127) / 128, tblks = (M + 8 * nt - 1) / (8 * nt);
   Args a{};
   a.sf = sfw;
   a.gs = gs_w;
   a.N = N;
   a.K = K;
-  a.xf = base + L.xf;
-  a.exps = reinterpret_cast<const int32_t*>(base + L.exps);
+  a.x = x;
+  a.ld_bytes = ld * 2;
   a.M = static_cast<int>(M);
   a.out = out;
   a.out_f32 = out_dtype == 0;
-  a.splits = pick_splits(rowblks * tblks, K, kMaxSplits);
+  a.splits = P.splits;
   a.status = dev_status;
-  return launch_nt<DENSE>(
-      nt, w, N, a,
-      dim3(static_cast<unsigned>(rowblks * a.splits), static_cast<unsigned>(tblks)), s);
+  const dim3 grid(static_cast<unsigned>(P.rowblks * P.splits), static_cast<unsigned>(P.tblks));
+  if (P.xin) {
+    CUtensorMap tm;
+    if (!weight_map(&tm, w, N, K)) return NVFP4_ERR_CUDA;
+    return launch<1, DENSE, true>(tm, a, grid, false, s);
+  }
+  a.xf = base;
+  a.exps = reinterpret_cast<const int32_t*>(base + P.exps);
+  convert_kernel<false><<<static_cast<unsigned>(M), 256, 0, s>>>(
+      x, ld * 2, K, base, reinterpret_cast<int32_t*>(base + P.exps));
+  const nvfp4_status_t st = check_launch("convert_kernel");
+  if (st != NVFP4_OK) return st;
+  return launch_nt<DENSE>(P.nt, w, N, a, grid, s);
 }
 
 extern "C" size_t moe_ffn_w4a16_workspace_size(int T, int H, int I, int E, int k) {
@@ -887,7 +986,7 @@ extern "C" nvfp4_status_t moe_ffn_w4a16(const void* x_bf16, const float* logits,
   st = launch_nt<FFN_L1>(nt, w1, (int64_t)E * 2 * I, a, dim3(blocks1 * a.splits, busy), s);
   if (st != NVFP4_OK) return st;
   st = launch_after(
-      convert_kernel<true>, dim3(S), 256, 0, 1, s, "convert_kernel", f32(L.h), (int64_t)I * 4, I,
+      convert_kernel<true>, dim3(S), 256, 0, 1, true, s, "convert_kernel", f32(L.h), (int64_t)I * 4, I,
       base + L.hf, i32(L.hexp));
   if (st != NVFP4_OK) return st;
   a.sf = sfw2;
@@ -902,6 +1001,6 @@ extern "C" nvfp4_status_t moe_ffn_w4a16(const void* x_bf16, const float* logits,
   st = launch_nt<FFN_L2>(nt, w2, (int64_t)E * H, a, dim3(blocks2 * a.splits, busy), s);
   if (st != NVFP4_OK) return st;
   return launch_after(
-      combine_slots_kernel, dim3(T, (H / 4 + 255) / 256), 256, 0, 1, s, "combine_slots_kernel",
+      combine_slots_kernel, dim3(T, (H / 4 + 255) / 256), 256, 0, 1, true, s, "combine_slots_kernel",
       f32(L.ys), ids, wts, H, E, k, static_cast<__nv_bfloat16*>(out_bf16));
 }
