@@ -561,6 +561,51 @@ NVFP4_API nvfp4_status_t moe_ffn_w4a16(const void* x_bf16, const float* logits,
                                        nvfp4_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------------
+ * moe_balance_loss — the router's load-balance loss, the per-expert counts, and (optionally, in the
+ * same pass) the gradient with respect to the logits.
+ * moe_balance_loss_backward — that gradient alone, from the counts of an earlier call.
+ *
+ *   sequence s holds the tokens seq_offs[s] <= t < seq_offs[s+1] whose mask is not 0, n_s of them;
+ *   c[s][e] of their k slots name expert e; p_t = softmax(logits_t); f[s][e] = E c[s][e] / (k n_s)
+ *   loss = alpha / S' * sum_s sum_e f[s][e] * mean over the sequence's tokens of p_t[e]
+ *          (S' = sequences with n_s > 0; 0 when there are none)
+ *   dlogits_t[e] = dloss * alpha / (S' n_s) * p_t[e] * (f[s][e] - sum_j f[s][j] p_t[j])
+ *   The counts are constants of the gradient.  A perfectly even load gives loss = alpha.
+ *
+ *   logits    float [T][ld] (ld >= E); a -inf logit has probability 0 and no gradient, a row of
+ *             nothing but -inf has no probabilities at all (its token still counts in n_s)
+ *   topk_ids  int32 [T][k] from moe_permute (or any router); < 0: dropped, >= E: dropped and
+ *             NVFP4_DEVERR_BAD_INDEX
+ *   seq_offs  device int32 [S+1], ascending, within [0, T] (else NVFP4_DEVERR_BAD_OFFSETS, and the
+ *             offsets are clamped); NULL with S = 1: one sequence of all T tokens.  Tokens before
+ *             the first or behind the last sequence count in none.
+ *   mask      uint8 [T] or NULL: 0 = a padding token, which counts in none.  Whatever its logits
+ *             hold, it adds nothing, and its gradient row is zero.
+ *   counts    int32 [S][E] and tokens int32 [S] (n_s): outputs, inputs of the backward call
+ *   loss      device float[1]
+ *   dloss     device float[1] or NULL (1): gradient of the loss
+ *   dlogits   float [T][E] or NULL, not overlapping logits; accumulate != 0: added to what it
+ *             holds (such as the gradient that came through the routing weights)
+ *   ws        device scratch of moe_balance_loss_workspace_size(T, E) bytes, 16-byte aligned
+ *   The loss is added up in float64 in a fixed order (reproducible).
+ *   Constraints: 1 <= k <= E <= 256, k <= 32, T*k <= 2^30, 1 <= S <= 2^24.
+ * ------------------------------------------------------------------------------------------- */
+NVFP4_API size_t moe_balance_loss_workspace_size(int T, int E);
+NVFP4_API nvfp4_status_t moe_balance_loss(const float* logits, int64_t ld, int T, int E, int k,
+                                          const int32_t* topk_ids, const int32_t* seq_offs, int S,
+                                          const uint8_t* mask, float alpha, int32_t* counts,
+                                          int32_t* tokens, float* loss, const float* dloss,
+                                          float* dlogits, int accumulate, void* ws,
+                                          size_t ws_bytes, int32_t* dev_status,
+                                          nvfp4_stream_t stream);
+NVFP4_API nvfp4_status_t moe_balance_loss_backward(const float* logits, int64_t ld, int T, int E,
+                                                   int k, const int32_t* counts,
+                                                   const int32_t* tokens, const int32_t* seq_offs,
+                                                   int S, const uint8_t* mask, float alpha,
+                                                   const float* dloss, float* dlogits,
+                                                   int accumulate, nvfp4_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
  * Status helpers.
  *   nvfp4_read_status: copies *dev_status to *host_code (host pointer) on `stream` and waits for
  *   the stream; returns NVFP4_ERR_TIMEOUT / NVFP4_ERR_BAD_INDEX when the matching bit is set.

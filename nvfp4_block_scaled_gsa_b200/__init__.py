@@ -7,6 +7,8 @@ tensors and the current CUDA stream into its calls.
 
 from .api import (  # noqa: F401
     NVFP4Weights,
+    balance_loss,
+    balance_loss_backward,
     ffn_workspace_bytes,
     gemm_dense,
     grouped_gemm,

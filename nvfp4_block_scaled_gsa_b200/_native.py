@@ -84,6 +84,13 @@ SIGNATURES = {
     "moe_ffn_w4a16": (c_int, [c_void, c_void, c_void, c_void, c_int, c_int, c_int, c_int, c_int,
                               c_void, c_void, c_void, c_void, c_void, c_void, c_void, c_void,
                               c_size, c_void, c_void]),
+    "moe_balance_loss_workspace_size": (c_size, [c_int, c_int]),
+    "moe_balance_loss": (c_int, [c_void, c_i64, c_int, c_int, c_int, c_void, c_void, c_int, c_void,
+                                 c_float, c_void, c_void, c_void, c_void, c_void, c_int, c_void,
+                                 c_size, c_void, c_void]),
+    "moe_balance_loss_backward": (c_int, [c_void, c_i64, c_int, c_int, c_int, c_void, c_void,
+                                          c_void, c_int, c_void, c_float, c_void, c_void, c_int,
+                                          c_void]),
     "nvfp4_read_status": (c_int, [c_void, c_void, c_void]),
     "nvfp4_wait_selftest": (c_int, [c_i64, c_void, c_void, c_void]),
     "nvfp4_last_error": (c_char_p, []),

@@ -455,6 +455,71 @@ def moe_ffn_w4a16(x, logits, k, w1: NVFP4Weights, w2: NVFP4Weights, ids=None, we
     return out
 
 
+def _balance_operands(logits, seq_offs, mask, dloss, dlogits, status):
+    """Checks shared by the balance loss and its gradient; returns (T, E, sequences)."""
+    assert logits.dtype == F32 and logits.dim() == 2 and logits.stride(1) == 1
+    T, E = logits.shape
+    _same_device(logits.device, seq_offs, mask, dloss, dlogits, status)
+    S = 1
+    if seq_offs is not None:
+        assert seq_offs.dtype == I32 and seq_offs.dim() == 1 and seq_offs.is_contiguous()
+        S = seq_offs.numel() - 1
+    if mask is not None:
+        assert mask.dtype in (torch.bool, U8) and mask.shape == (T,) and mask.is_contiguous()
+    if dloss is not None:
+        assert dloss.dtype == F32 and dloss.numel() == 1
+    if dlogits is not None:
+        assert dlogits.dtype == F32 and dlogits.shape == (T, E) and dlogits.is_contiguous()
+    return T, E, S
+
+
+def balance_loss(logits, ids, alpha, seq_offs=None, mask=None, want_grad=False, dloss=None,
+                 dlogits=None, ws=None, status=None):
+    """The router's load-balance loss: alpha / S' * sum over the S' sequences that hold tokens of
+    E * sum_e (share of their slots on e) * (mean softmax(logits)[e]).
+
+    logits float32 (T, E) (rows may be strided), ids int32 (T, k) from permute().  seq_offs int32
+    (S+1,): packed sequences (default: one of all tokens); mask (T,) bool or uint8: False/0 for
+    padding tokens.  Returns (loss (1,), counts int32 (S, E), tokens int32 (S,), dlogits or
+    None).  want_grad: dlogits (T, E) float32, times dloss (device float[1], default 1), in the
+    same pass; a given dlogits is added to."""
+    accumulate = dlogits is not None
+    T, E, S = _balance_operands(logits, seq_offs, mask, dloss, dlogits, status)
+    dev = logits.device
+    _same_device(dev, ids, ws)
+    assert ids.dtype == I32 and ids.dim() == 2 and ids.shape[0] == T and ids.is_contiguous()
+    k = ids.shape[1]
+    meta = torch.empty(S * E + S + 1, dtype=I32, device=dev)
+    counts, tokens = meta[:S * E].view(S, E), meta[S * E:S * E + S]
+    loss = meta[S * E + S:].view(F32)
+    if want_grad and dlogits is None:
+        dlogits = torch.empty(T, E, dtype=F32, device=dev)
+    if ws is None:
+        ws = torch.empty(int(lib().moe_balance_loss_workspace_size(T, E)), dtype=U8, device=dev)
+    _call_on(dev, "moe_balance_loss", _p(logits), _row_stride(logits), T, E, k, _p(ids),
+             _p(seq_offs), S, _p(mask), float(alpha), _p(counts), _p(tokens), _p(loss), _p(dloss),
+             _p(dlogits), int(accumulate), _p(ws), _bytes(ws), _p(status))
+    return loss, counts, tokens, dlogits
+
+
+def balance_loss_backward(logits, counts, tokens, k, alpha, dloss=None, seq_offs=None, mask=None,
+                          dlogits=None):
+    """The gradient of balance_loss with respect to the logits, from its counts and tokens: float32
+    (T, E), times dloss (device float[1], default 1).  A given dlogits is added to."""
+    accumulate = dlogits is not None
+    T, E, S = _balance_operands(logits, seq_offs, mask, dloss, dlogits, None)
+    dev = logits.device
+    _same_device(dev, counts, tokens)
+    assert counts.dtype == I32 and counts.shape == (S, E) and counts.is_contiguous()
+    assert tokens.dtype == I32 and tokens.shape == (S,) and tokens.is_contiguous()
+    if dlogits is None:
+        dlogits = torch.empty(T, E, dtype=F32, device=dev)
+    _call_on(dev, "moe_balance_loss_backward", _p(logits), _row_stride(logits), T, E, k,
+             _p(counts), _p(tokens), _p(seq_offs), S, _p(mask), float(alpha), _p(dloss),
+             _p(dlogits), int(accumulate))
+    return dlogits
+
+
 def read_status(status):
     """Host copy of a device status word (synchronizes the current stream)."""
     host = torch.zeros(1, dtype=torch.int32)

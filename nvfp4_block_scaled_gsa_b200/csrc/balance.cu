@@ -1,0 +1,474 @@
+// balance.cu — the router's load-balance loss with its per-expert counts and its gradient.
+//
+// Over the tokens of sequence s that count (n_s of them), with c[s][e] of their k slots routed to
+// expert e, p_t = softmax(logits_t) and S' sequences that hold a token:
+//
+//   f[s][e] = E c[s][e] / (k n_s)
+//   loss    = alpha / S' * sum_s sum_e f[s][e] * (1/n_s) sum_{t in s} p_t[e]
+//           = sum_t a_s v_t,   a_s = alpha / (S' n_s),  v_t = sum_e f[s][e] p_t[e]
+//   dlogits_t[e] = dloss * a_s * p_t[e] * (f[s][e] - v_t)        (the counts have no gradient)
+//
+// With the counts known the loss is a sum over tokens of the same v_t that the gradient needs, so
+// one pass over the logits gives both; no mean probability per expert is ever formed.  Two launches:
+// the counts from the ids (a cluster per sequence, its CTAs' histograms joined through distributed
+// shared memory, nothing to zero), and the pass, which loads its first logits while the counts
+// are still being made.  Bound by reading the logits and writing their gradient.
+#include "common.cuh"
+#include "launch.h"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kMaxE = 256;
+constexpr int kMaxK = 32;
+constexpr int kCountThreads = 512;
+constexpr int kCountCluster = 8;  // CTAs per sequence, up to kClusterSeqs sequences
+constexpr int kClusterSeqs = 64;
+constexpr int kThreads = 256;
+constexpr int kSlots = 8;         // logits a lane holds
+// CTAs of the pass, at most: the 4 that an SM holds on each of the 148 (more than one round of
+// CTAs would pay for the start, three dependent loads, again)
+constexpr int kMaxCtas = 148 * 4;
+constexpr int kOffsCache = 1024;  // sequence offsets kept in shared memory, at most
+
+__device__ __forceinline__ int clamp_to(int v, int lo, int hi) { return min(max(v, lo), hi); }
+
+// Counts of one sequence by the CTAs of a cluster (or one CTA).
+__global__ void __launch_bounds__(kCountThreads) balance_count_kernel(
+    const int32_t* __restrict__ ids, int T, int E, int k, const int32_t* __restrict__ seq_offs,
+    const uint8_t* __restrict__ mask, int cluster, int32_t* __restrict__ counts,
+    int32_t* __restrict__ tokens, uint32_t* __restrict__ ticket, int32_t* __restrict__ dev_status) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ int hist[kMaxE + 1];  // [E]: the tokens
+  const int tid = threadIdx.x;
+  const int s = blockIdx.x / cluster, rank = blockIdx.x % cluster;
+  for (int e = tid; e <= E; e += kCountThreads) hist[e] = 0;
+  if (blockIdx.x == 0 && tid == 0 && ticket != nullptr) *ticket = 0;
+  int lo = 0, hi = T;
+  bool bad = false;
+  if (seq_offs != nullptr) {
+    const int a = __ldg(seq_offs + s), b = __ldg(seq_offs + s + 1);
+    lo = clamp_to(a, 0, T);
+    hi = clamp_to(b, lo, T);
+    if (a != lo || b != hi) report(dev_status, NVFP4_DEVERR_BAD_OFFSETS);
+  }
+  __syncthreads();
+  // this CTA's part of the sequence's tokens, and their slots (T * k < 2^30: 32-bit indices)
+  const int n = hi - lo, per = (n + cluster - 1) / cluster;
+  const int t0 = lo + min(n, per * rank), t1 = lo + min(n, per * (rank + 1));
+  int held = 0;
+  if (mask == nullptr) {
+    held = tid == 0 ? t1 - t0 : 0;
+  } else {
+    for (int t = t0 + tid; t < t1; t += kCountThreads) held += __ldg(mask + t) != 0;
+  }
+  held = __reduce_add_sync(0xffffffffu, held);
+  if ((tid & 31) == 0 && held) atomicAdd(&hist[E], held);
+  constexpr int kAhead = 8;
+  const int j1 = t1 * k;
+  for (int j = t0 * k + tid; j < j1; j += kCountThreads * kAhead) {
+    int id[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int at = j + u * kCountThreads;
+      id[u] = -1;
+      if (at < j1 && (mask == nullptr || __ldg(mask + static_cast<unsigned>(at) / static_cast<unsigned>(k)) != 0))
+        id[u] = __ldg(ids + at);
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (id[u] >= E) bad = true;
+      else if (id[u] >= 0) atomicAdd(&hist[id[u]], 1);
+    }
+  }
+  if (bad) report(dev_status, NVFP4_DEVERR_BAD_INDEX);
+  if (cluster > 1) cluster_sync();
+  else __syncthreads();
+  for (int e = rank * kCountThreads + tid; e <= E; e += cluster * kCountThreads) {
+    int sum = 0;
+    if (cluster > 1) {
+      const uint32_t at = smem_u32(&hist[e]);
+      for (int c = 0; c < cluster; ++c) {
+        int v;
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(at, c)) : "memory");
+        sum += v;
+      }
+    } else {
+      sum = hist[e];
+    }
+    if (e < E) counts[(int64_t)s * E + e] = sum;
+    else tokens[s] = sum;
+  }
+  if (cluster > 1) cluster_sync();  // the peers have read this CTA's histogram
+}
+
+struct Args {
+  const float* logits;
+  int64_t ld;
+  int T, E, k;
+  const int32_t* seq_offs;
+  int S;
+  const uint8_t* mask;
+  float alpha;
+  const int32_t* counts;
+  const int32_t* tokens;
+  const float* dloss;
+  float* dlogits;
+  int accumulate;
+  float* loss;
+  double* part;      // [CTAs]
+  uint32_t* ticket;  // zero when the CTAs start to finish
+  int iters;         // groups of 32 / L tokens per warp
+};
+
+__device__ __forceinline__ int32_t ld_after(const int32_t* p) {
+  int32_t v;
+  asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
+// L lanes per token, up to 8 logits each; a warp takes 32 / L consecutive tokens at a time.  VEC:
+// a lane's logits are two 16-byte groups (E % 4 == 0 and rows 16-byte aligned), else 8 words L
+// apart.
+template <int L, bool VEC>
+__global__ void __launch_bounds__(kThreads, 4) balance_kernel(const Args A) {
+  constexpr int G = 32 / L;
+  const int tid = threadIdx.x, lane = tid & 31, l = lane % L, grp = lane / L;
+  const int E = A.E;
+  auto expert = [&](int i) { return VEC ? 4 * (l + L * (i >> 2)) + (i & 3) : l + L * i; };
+  const int64_t warp = (int64_t)blockIdx.x * (kThreads / 32) + (tid >> 5);
+  const int64_t t_first = warp * A.iters * G + grp;
+  auto load = [&](int64_t t, float (&v)[kSlots]) {
+    const float* row = A.logits + t * A.ld;
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < kSlots; i += 4) {
+        float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t < A.T && expert(i) < E) q = __ldg(reinterpret_cast<const float4*>(row + expert(i)));
+        v[i] = q.x;
+        v[i + 1] = q.y;
+        v[i + 2] = q.z;
+        v[i + 3] = q.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i)
+        v[i] = t < A.T && expert(i) < E ? __ldg(row + expert(i)) : 0.0f;
+    }
+  };
+  auto masked = [&](int64_t t) {
+    return A.mask != nullptr && t < A.T && __ldg(A.mask + t) == 0;
+  };
+  float v[kSlots];
+  load(t_first, v);
+  bool skip = masked(t_first);
+  __shared__ int s_busy, s_offs[kOffsCache];
+  const int* offs = A.seq_offs;
+  if (A.S < kOffsCache) {
+    for (int s = tid; s <= A.S; s += kThreads)
+      s_offs[s] = A.seq_offs == nullptr ? (s == 0 ? 0 : A.T) : __ldg(A.seq_offs + s);
+    offs = s_offs;
+  }
+  if (tid == 0) s_busy = 0;
+  __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the counts
+
+  // sequences that hold a token
+  int busy = 0;
+  for (int s = tid; s < A.S; s += kThreads) busy += ld_after(A.tokens + s) > 0;
+  busy = __reduce_add_sync(0xffffffffu, busy);
+  if (lane == 0 && busy) atomicAdd(&s_busy, busy);
+  const float up = A.dloss != nullptr ? __ldg(A.dloss) : 1.0f;
+  __syncthreads();
+  const float a_all = s_busy > 0 ? A.alpha / static_cast<float>(s_busy) : 0.0f;
+
+  // the sequence of the group's current token: the last that starts at or before it
+  int s = -1, s_end = 0;
+  bool inside = false;  // a sequence with tokens
+  float f[kSlots], coef = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) f[i] = 0.0f;
+  auto enter = [&](int64_t t) {
+    int lo = max(s, 0), hi = A.S;
+    if (t >= offs[hi] || t < offs[lo]) {
+      inside = false;
+      s_end = t < offs[lo] ? offs[lo] : A.T;
+      return;
+    }
+    while (hi - lo > 1) {  // offs[lo] <= t < offs[hi]
+      const int mid = (lo + hi) / 2;
+      if (offs[mid] <= t) lo = mid;
+      else hi = mid;
+    }
+    s = lo;
+    s_end = offs[lo + 1];
+    const int n = ld_after(A.tokens + s);
+    int c[kSlots];
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i)
+      c[i] = expert(i) < E ? ld_after(A.counts + (int64_t)s * E + expert(i)) : 0;
+    inside = n > 0;
+    coef = inside ? a_all / static_cast<float>(n) : 0.0f;
+    const float unit =
+        inside ? static_cast<float>(E) / (static_cast<float>(A.k) * static_cast<float>(n)) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) f[i] = static_cast<float>(c[i]) * unit;
+  };
+
+  double sum = 0.0;
+  for (int it = 0; it < A.iters; ++it) {
+    const int64_t t = t_first + (int64_t)it * G;
+    if (t - grp >= A.T) break;  // the whole warp
+    float nxt[kSlots];
+    bool nxt_skip = false;
+    if (it + 1 < A.iters) {
+      load(t + G, nxt);
+      nxt_skip = masked(t + G);
+    }
+    if (t < A.T && t >= s_end) enter(t);
+    const bool counted = t < A.T && inside && !skip;
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i)
+      if (expert(i) < E) m = fmaxf(m, v[i]);
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float z = 0.0f, dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+      // a row of nothing but -inf has no probabilities
+      v[i] = expert(i) < E && !(m == -INFINITY && v[i] == -INFINITY) ? expf(v[i] - m) : 0.0f;
+      z += v[i];
+      dot += v[i] * f[i];
+    }
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) {
+      z += __shfl_xor_sync(0xffffffffu, z, o);
+      dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    }
+    const float inv = z == 0.0f ? 0.0f : 1.0f / z;
+    const float vt = dot * inv;
+    if (counted && l == 0) sum += static_cast<double>(coef) * static_cast<double>(vt);
+    if (A.dlogits != nullptr && t < A.T) {
+      float* row = A.dlogits + t * E;
+      const float scale = counted ? up * coef * inv : 0.0f;
+      float d[kSlots];
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i) d[i] = counted ? scale * v[i] * (f[i] - vt) : 0.0f;
+      if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < kSlots; i += 4) {
+          if (expert(i) >= E) continue;
+          float4* at = reinterpret_cast<float4*>(row + expert(i));
+          float4 o = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
+          if (A.accumulate) {
+            const float4 was = *at;
+            o.x += was.x;
+            o.y += was.y;
+            o.z += was.z;
+            o.w += was.w;
+          }
+          *at = o;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i)
+          if (expert(i) < E) row[expert(i)] = A.accumulate ? row[expert(i)] + d[i] : d[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) v[i] = nxt[i];
+    skip = nxt_skip;
+  }
+
+  if (A.loss == nullptr) return;
+  // one float64 sum per CTA; the CTA that finishes last adds them in order
+  __shared__ double s_sum[kThreads / 32];
+  __shared__ bool s_last;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) s_sum[tid >> 5] = sum;
+  __syncthreads();
+  if (tid == 0) {
+    double total = 0.0;
+    for (int w = 0; w < kThreads / 32; ++w) total += s_sum[w];
+    A.part[blockIdx.x] = total;
+    __threadfence();
+    s_last = atomicAdd(A.ticket, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  double total = 0.0;
+  constexpr int kPer = (kMaxCtas + kThreads - 1) / kThreads;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int c = tid + j * kThreads;
+    if (c < static_cast<int>(gridDim.x)) total += __ldcg(A.part + c);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (lane == 0) s_sum[tid >> 5] = total;
+  __syncthreads();
+  if (tid == 0) {
+    total = 0.0;
+    for (int w = 0; w < kThreads / 32; ++w) total += s_sum[w];
+    *A.loss = static_cast<float>(total);
+  }
+}
+
+int lanes_for(int E) {
+  int L = 2;
+  while (kSlots * L < E) L *= 2;
+  return L;
+}
+
+// iters (token groups per warp) and the grid of the pass
+void pass_shape(int T, int E, int& iters, int& ctas) {
+  const int G = 32 / lanes_for(E), warps = kThreads / 32;
+  const int64_t groups = ((int64_t)T + G - 1) / G;
+  const int64_t most = (int64_t)kMaxCtas * warps;
+  iters = static_cast<int>((groups + most - 1) / most);
+  if (iters < 1) iters = 1;
+  const int64_t per_cta = (int64_t)iters * warps;
+  ctas = static_cast<int>((groups + per_cta - 1) / per_cta);
+  if (ctas < 1) ctas = 1;
+}
+
+template <int L>
+nvfp4_status_t launch_pass(Args& a, bool vec, bool early, cudaStream_t s) {
+  int ctas;
+  pass_shape(a.T, a.E, a.iters, ctas);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = early ? 1 : 0;
+  if (vec) cudaLaunchKernelEx(&cfg, balance_kernel<L, true>, static_cast<const Args>(a));
+  else cudaLaunchKernelEx(&cfg, balance_kernel<L, false>, static_cast<const Args>(a));
+  return check_launch("balance_kernel");
+}
+
+nvfp4_status_t pass(Args& a, bool early, cudaStream_t s) {
+  const bool vec = a.E % 4 == 0 && a.ld % 4 == 0 && aligned16(a.logits) && aligned16(a.dlogits);
+  switch (lanes_for(a.E)) {
+    case 2: return launch_pass<2>(a, vec, early, s);
+    case 4: return launch_pass<4>(a, vec, early, s);
+    case 8: return launch_pass<8>(a, vec, early, s);
+    case 16: return launch_pass<16>(a, vec, early, s);
+    default: return launch_pass<32>(a, vec, early, s);
+  }
+}
+
+constexpr int64_t kPartOffset = 256;  // workspace: the ticket, then a float64 per CTA
+
+nvfp4_status_t check_shape(int T, int E, int k, int64_t ld, int S, const int32_t* seq_offs) {
+  if (T < 0 || E < 1 || k < 1 || ld < E || S < 1) return NVFP4_ERR_INVALID_ARG;
+  if (E > kMaxE || k > kMaxK || k > E || (int64_t)T * k > (int64_t)1 << 30 || S > (1 << 24))
+    return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (seq_offs == nullptr && S != 1) return NVFP4_ERR_INVALID_ARG;
+  return NVFP4_OK;
+}
+
+}  // namespace
+}  // namespace nvfp4
+
+using namespace nvfp4;
+
+extern "C" size_t moe_balance_loss_workspace_size(int T, int E) {
+  if (T < 0 || E < 1 || E > kMaxE) return 0;
+  int iters, ctas;
+  pass_shape(T, E, iters, ctas);
+  return static_cast<size_t>(kPartOffset + (int64_t)ctas * 8);
+}
+
+extern "C" nvfp4_status_t moe_balance_loss(const float* logits, int64_t ld, int T, int E, int k,
+                                           const int32_t* topk_ids, const int32_t* seq_offs, int S,
+                                           const uint8_t* mask, float alpha, int32_t* counts,
+                                           int32_t* tokens, float* loss, const float* dloss,
+                                           float* dlogits, int accumulate, void* ws,
+                                           size_t ws_bytes, int32_t* dev_status,
+                                           nvfp4_stream_t stream) {
+  nvfp4_status_t st = check_shape(T, E, k, ld, S, seq_offs);
+  if (st != NVFP4_OK) return st;
+  if (!counts || !tokens || !loss || !ws) return NVFP4_ERR_INVALID_ARG;
+  if (T > 0 && (!logits || !topk_ids)) return NVFP4_ERR_INVALID_ARG;
+  if (ws_bytes < moe_balance_loss_workspace_size(T, E)) return NVFP4_ERR_WORKSPACE_TOO_SMALL;
+  const void* ptrs4[] = {logits, topk_ids, seq_offs, counts, tokens, loss, dloss, dlogits, dev_status};
+  for (const void* p : ptrs4)
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return NVFP4_ERR_MISALIGNED;
+  if (!aligned16(ws)) return NVFP4_ERR_MISALIGNED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  uint32_t* ticket = reinterpret_cast<uint32_t*>(base);
+  const int cluster = S <= kClusterSeqs ? kCountCluster : 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(S * cluster));
+  cfg.blockDim = dim3(kCountThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = static_cast<unsigned>(cluster);
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, balance_count_kernel, topk_ids, T, E, k, seq_offs, mask, cluster, counts,
+                     tokens, ticket, dev_status);
+  st = check_launch("balance_count_kernel");
+  if (st != NVFP4_OK) return st;
+  Args a{};
+  a.logits = logits;
+  a.ld = ld;
+  a.T = T;
+  a.E = E;
+  a.k = k;
+  a.seq_offs = seq_offs;
+  a.S = S;
+  a.mask = mask;
+  a.alpha = alpha;
+  a.counts = counts;
+  a.tokens = tokens;
+  a.dloss = dloss;
+  a.dlogits = dlogits;
+  a.accumulate = accumulate;
+  a.loss = loss;
+  a.part = reinterpret_cast<double*>(base + kPartOffset);
+  a.ticket = ticket;
+  return pass(a, true, s);
+}
+
+extern "C" nvfp4_status_t moe_balance_loss_backward(const float* logits, int64_t ld, int T, int E,
+                                                    int k, const int32_t* counts,
+                                                    const int32_t* tokens, const int32_t* seq_offs,
+                                                    int S, const uint8_t* mask, float alpha,
+                                                    const float* dloss, float* dlogits,
+                                                    int accumulate, nvfp4_stream_t stream) {
+  const nvfp4_status_t st = check_shape(T, E, k, ld, S, seq_offs);
+  if (st != NVFP4_OK) return st;
+  if (!counts || !tokens) return NVFP4_ERR_INVALID_ARG;
+  if (T > 0 && (!logits || !dlogits)) return NVFP4_ERR_INVALID_ARG;
+  const void* ptrs4[] = {logits, seq_offs, counts, tokens, dloss, dlogits};
+  for (const void* p : ptrs4)
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return NVFP4_ERR_MISALIGNED;
+  if (T == 0) return NVFP4_OK;
+  Args a{};
+  a.logits = logits;
+  a.ld = ld;
+  a.T = T;
+  a.E = E;
+  a.k = k;
+  a.seq_offs = seq_offs;
+  a.S = S;
+  a.mask = mask;
+  a.alpha = alpha;
+  a.counts = counts;
+  a.tokens = tokens;
+  a.dloss = dloss;
+  a.dlogits = dlogits;
+  a.accumulate = accumulate;
+  return pass(a, false, reinterpret_cast<cudaStream_t>(stream));
+}
