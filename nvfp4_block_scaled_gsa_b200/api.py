@@ -367,8 +367,9 @@ def _call_on(dev, name, *args):
 
 def _same_device(dev, *tensors):
     assert dev.type == "cuda", "CUDA tensors only"
+    index = dev.index
     for t in tensors:
-        assert t is None or t.device == dev, f"all tensors must be on {dev}"
+        assert t is None or t.get_device() == index, f"all tensors must be on {dev}"
 
 
 def _check_weights(w: "NVFP4Weights", dev):
@@ -489,9 +490,9 @@ def balance_loss(logits, ids, alpha, seq_offs=None, mask=None, want_grad=False, 
     _same_device(dev, ids, ws)
     assert ids.dtype == I32 and ids.dim() == 2 and ids.shape[0] == T and ids.is_contiguous()
     k = ids.shape[1]
-    meta = torch.empty(S * E + S + 1, dtype=I32, device=dev)
-    counts, tokens = meta[:S * E].view(S, E), meta[S * E:S * E + S]
-    loss = meta[S * E + S:].view(F32)
+    counts = torch.empty(S, E, dtype=I32, device=dev)
+    tokens = torch.empty(S, dtype=I32, device=dev)
+    loss = torch.empty(1, dtype=F32, device=dev)
     if want_grad and dlogits is None:
         dlogits = torch.empty(T, E, dtype=F32, device=dev)
     if ws is None:

@@ -25,10 +25,9 @@ constexpr int kCountThreads = 512;
 constexpr int kCountCluster = 8;  // CTAs per sequence, up to kClusterSeqs sequences
 constexpr int kClusterSeqs = 64;
 constexpr int kThreads = 256;
-constexpr int kSlots = 8;         // logits a lane holds
-// CTAs of the pass, at most: the 4 that an SM holds on each of the 148 (more than one round of
+// CTAs of the pass, at most: the 3 that an SM holds on each of the 148 (more than one round of
 // CTAs would pay for the start, three dependent loads, again)
-constexpr int kMaxCtas = 148 * 4;
+constexpr int kMaxCtas = 148 * 3;
 constexpr int kOffsCache = 1024;  // sequence offsets kept in shared memory, at most
 
 __device__ __forceinline__ int clamp_to(int v, int lo, int hi) { return min(max(v, lo), hi); }
@@ -64,7 +63,7 @@ __global__ void __launch_bounds__(kCountThreads) balance_count_kernel(
   }
   held = __reduce_add_sync(0xffffffffu, held);
   if ((tid & 31) == 0 && held) atomicAdd(&hist[E], held);
-  constexpr int kAhead = 8;
+  constexpr int kAhead = 16;
   const int j1 = t1 * k;
   for (int j = t0 * k + tid; j < j1; j += kCountThreads * kAhead) {
     int id[kAhead];
@@ -86,13 +85,17 @@ __global__ void __launch_bounds__(kCountThreads) balance_count_kernel(
   else __syncthreads();
   for (int e = rank * kCountThreads + tid; e <= E; e += cluster * kCountThreads) {
     int sum = 0;
-    if (cluster > 1) {
+    if (cluster > 1) {  // kCountCluster CTAs, their words in flight together
       const uint32_t at = smem_u32(&hist[e]);
-      for (int c = 0; c < cluster; ++c) {
-        int v;
-        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(at, c)) : "memory");
-        sum += v;
-      }
+      int v[kCountCluster];
+#pragma unroll
+      for (int c = 0; c < kCountCluster; ++c)
+        asm volatile("ld.shared::cluster.s32 %0, [%1];"
+                     : "=r"(v[c])
+                     : "r"(mapa_shared(at, c))
+                     : "memory");
+#pragma unroll
+      for (int c = 0; c < kCountCluster; ++c) sum += v[c];
     } else {
       sum = hist[e];
     }
@@ -127,23 +130,25 @@ __device__ __forceinline__ int32_t ld_after(const int32_t* p) {
   return v;
 }
 
-// L lanes per token, up to 8 logits each; a warp takes 32 / L consecutive tokens at a time.  VEC:
-// a lane's logits are two 16-byte groups (E % 4 == 0 and rows 16-byte aligned), else 8 words L
-// apart.
-template <int L, bool VEC>
-__global__ void __launch_bounds__(kThreads, 4) balance_kernel(const Args A) {
-  constexpr int G = 32 / L;
+// L lanes per token, 4 * NV logits each; a warp takes 32 / L consecutive tokens at a time.  Many
+// logits per lane keep the shuffles of the row sums few (40961 x 160 at 32 lanes of 8 was bound by
+// instruction issue: 297 a token; 18.4 us against TBD).  VEC: a lane's logits are NV 16-byte
+// groups (E % 4 == 0 and rows 16-byte aligned), else words L apart.
+template <int L, int NV, bool VEC>
+__global__ void __launch_bounds__(kThreads, 3) balance_kernel(const Args A) {
+  constexpr int G = 32 / L, kSlots = 4 * NV;
   const int tid = threadIdx.x, lane = tid & 31, l = lane % L, grp = lane / L;
   const int E = A.E;
   auto expert = [&](int i) { return VEC ? 4 * (l + L * (i >> 2)) + (i & 3) : l + L * i; };
   const int64_t warp = (int64_t)blockIdx.x * (kThreads / 32) + (tid >> 5);
   const int64_t t_first = warp * A.iters * G + grp;
+  // logits past E, and tokens past T, read as -inf: probability 0
   auto load = [&](int64_t t, float (&v)[kSlots]) {
     const float* row = A.logits + t * A.ld;
     if constexpr (VEC) {
 #pragma unroll
       for (int i = 0; i < kSlots; i += 4) {
-        float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
         if (t < A.T && expert(i) < E) q = __ldg(reinterpret_cast<const float4*>(row + expert(i)));
         v[i] = q.x;
         v[i + 1] = q.y;
@@ -153,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 4) balance_kernel(const Args A) {
     } else {
 #pragma unroll
       for (int i = 0; i < kSlots; ++i)
-        v[i] = t < A.T && expert(i) < E ? __ldg(row + expert(i)) : 0.0f;
+        v[i] = t < A.T && expert(i) < E ? __ldg(row + expert(i)) : -INFINITY;
     }
   };
   auto masked = [&](int64_t t) {
@@ -162,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 4) balance_kernel(const Args A) {
   float v[kSlots];
   load(t_first, v);
   bool skip = masked(t_first);
-  __shared__ int s_busy, s_offs[kOffsCache];
+  __shared__ int s_busy, s_offs[kOffsCache], s_counts[kMaxE];
   const int* offs = A.seq_offs;
   if (A.S < kOffsCache) {
     for (int s = tid; s <= A.S; s += kThreads)
@@ -173,44 +178,59 @@ __global__ void __launch_bounds__(kThreads, 4) balance_kernel(const Args A) {
   __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the counts
 
-  // sequences that hold a token
-  int busy = 0;
-  for (int s = tid; s < A.S; s += kThreads) busy += ld_after(A.tokens + s) > 0;
-  busy = __reduce_add_sync(0xffffffffu, busy);
-  if (lane == 0 && busy) atomicAdd(&s_busy, busy);
-  const float up = A.dloss != nullptr ? __ldg(A.dloss) : 1.0f;
-  __syncthreads();
-  const float a_all = s_busy > 0 ? A.alpha / static_cast<float>(s_busy) : 0.0f;
-
-  // the sequence of the group's current token: the last that starts at or before it
-  int s = -1, s_end = 0;
-  bool inside = false;  // a sequence with tokens
-  float f[kSlots], coef = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kSlots; ++i) f[i] = 0.0f;
-  auto enter = [&](int64_t t) {
-    int lo = max(s, 0), hi = A.S;
-    if (t >= offs[hi] || t < offs[lo]) {
-      inside = false;
-      s_end = t < offs[lo] ? offs[lo] : A.T;
-      return;
-    }
-    while (hi - lo > 1) {  // offs[lo] <= t < offs[hi]
+  // the last sequence that starts at or before t, given offs[lo] <= t < offs[S]
+  auto find = [&](int64_t t, int lo) {
+    int hi = A.S;
+    while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
       if (offs[mid] <= t) lo = mid;
       else hi = mid;
     }
-    s = lo;
-    s_end = offs[lo + 1];
-    const int n = ld_after(A.tokens + s);
-    int c[kSlots];
+    return lo;
+  };
+  // The counts of the sequence that the CTA's first token is in (or the first sequence) are read
+  // once per CTA: most CTAs lie in one sequence, and thousands of warps reading the same few lines
+  // would queue at one slice of L2 (8192 x 256: 16.6 us instead of TBD us for the pass).
+  const int64_t t_cta = (int64_t)blockIdx.x * (kThreads / 32) * A.iters * G;
+  const int s_cta = t_cta < offs[0] || t_cta >= offs[A.S] ? 0 : find(t_cta, 0);
+  int c_cta = 0, busy = 0;
+  if (tid < E) c_cta = ld_after(A.counts + (int64_t)s_cta * E + tid);
+  const int n_cta = ld_after(A.tokens + s_cta);
+  for (int j = tid; j < A.S; j += kThreads) busy += ld_after(A.tokens + j) > 0;
+  const float up = A.dloss != nullptr ? __ldg(A.dloss) : 1.0f;
+  busy = __reduce_add_sync(0xffffffffu, busy);
+  if (lane == 0 && busy) atomicAdd(&s_busy, busy);
+  if (tid < E) s_counts[tid] = c_cta;
+  __syncthreads();
+  const float share = s_busy > 0 ? 1.0f / static_cast<float>(s_busy) : 0.0f;
+
+  // the sequence of the group's current token
+  int s = -1, s_end = 0;
+  bool inside = false;  // a sequence with tokens
+  float f[kSlots], per_token = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kSlots; ++i)
-      c[i] = expert(i) < E ? ld_after(A.counts + (int64_t)s * E + expert(i)) : 0;
+  for (int i = 0; i < kSlots; ++i) f[i] = 0.0f;
+  auto enter = [&](int64_t t) {
+    const int lo = max(s, 0);
+    if (t >= offs[A.S] || t < offs[lo]) {
+      inside = false;
+      s_end = t < offs[lo] ? offs[lo] : A.T;
+      return;
+    }
+    s = find(t, lo);
+    s_end = offs[s + 1];
+    const int n = s == s_cta ? n_cta : ld_after(A.tokens + s);
     inside = n > 0;
-    coef = inside ? a_all / static_cast<float>(n) : 0.0f;
+    per_token = inside ? A.alpha / static_cast<float>(n) * share : 0.0f;
     const float unit =
         inside ? static_cast<float>(E) / (static_cast<float>(A.k) * static_cast<float>(n)) : 0.0f;
+    int c[kSlots];
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+      c[i] = 0;
+      if (expert(i) < E)
+        c[i] = s == s_cta ? s_counts[expert(i)] : ld_after(A.counts + (int64_t)s * E + expert(i));
+    }
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) f[i] = static_cast<float>(c[i]) * unit;
   };
@@ -227,17 +247,19 @@ __global__ void __launch_bounds__(kThreads, 4) balance_kernel(const Args A) {
     }
     if (t < A.T && t >= s_end) enter(t);
     const bool counted = t < A.T && inside && !skip;
-    float m = -INFINITY;
+    const float coef = per_token;
+    float m = v[0];
 #pragma unroll
-    for (int i = 0; i < kSlots; ++i)
-      if (expert(i) < E) m = fmaxf(m, v[i]);
+    for (int i = 1; i < kSlots; ++i) m = fmaxf(m, v[i]);
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (m == -INFINITY) m = 0.0f;  // a row of nothing but -inf: no probabilities
     float z = 0.0f, dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) {
-      // a row of nothing but -inf has no probabilities
-      v[i] = expert(i) < E && !(m == -INFINITY && v[i] == -INFINITY) ? expf(v[i] - m) : 0.0f;
+      // ex2.approx of the rounded argument: relative error about (2 + 1.4 |x|) * 2^-24, so at most
+      // 2^-23 of the row's sum of probabilities
+      v[i] = __expf(v[i] - m);
       z += v[i];
       dot += v[i] * f[i];
     }
@@ -246,15 +268,19 @@ __global__ void __launch_bounds__(kThreads, 4) balance_kernel(const Args A) {
       z += __shfl_xor_sync(0xffffffffu, z, o);
       dot += __shfl_xor_sync(0xffffffffu, dot, o);
     }
-    const float inv = z == 0.0f ? 0.0f : 1.0f / z;
+    const float inv = z == 0.0f ? 0.0f : __frcp_rn(z);
     const float vt = dot * inv;
     if (counted && l == 0) sum += static_cast<double>(coef) * static_cast<double>(vt);
     if (A.dlogits != nullptr && t < A.T) {
       float* row = A.dlogits + t * E;
-      const float scale = counted ? up * coef * inv : 0.0f;
+      const float scale = up * coef * inv;
       float d[kSlots];
 #pragma unroll
-      for (int i = 0; i < kSlots; ++i) d[i] = counted ? scale * v[i] * (f[i] - vt) : 0.0f;
+      for (int i = 0; i < kSlots; ++i) d[i] = scale * v[i] * (f[i] - vt);
+      if (!counted) {  // whatever the row holds
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) d[i] = 0.0f;
+      }
       if constexpr (VEC) {
 #pragma unroll
         for (int i = 0; i < kSlots; i += 4) {
@@ -317,9 +343,10 @@ __global__ void __launch_bounds__(kThreads, 4) balance_kernel(const Args A) {
   }
 }
 
+// The fewest lanes per token (2, 4, 8 or 16) that hold at most 16 logits each.
 int lanes_for(int E) {
   int L = 2;
-  while (kSlots * L < E) L *= 2;
+  while (16 * L < E) L *= 2;
   return L;
 }
 
@@ -335,7 +362,7 @@ void pass_shape(int T, int E, int& iters, int& ctas) {
   if (ctas < 1) ctas = 1;
 }
 
-template <int L>
+template <int L, int NV>
 nvfp4_status_t launch_pass(Args& a, bool vec, bool early, cudaStream_t s) {
   int ctas;
   pass_shape(a.T, a.E, a.iters, ctas);
@@ -348,19 +375,24 @@ nvfp4_status_t launch_pass(Args& a, bool vec, bool early, cudaStream_t s) {
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = early ? 1 : 0;
-  if (vec) cudaLaunchKernelEx(&cfg, balance_kernel<L, true>, static_cast<const Args>(a));
-  else cudaLaunchKernelEx(&cfg, balance_kernel<L, false>, static_cast<const Args>(a));
+  if (vec) cudaLaunchKernelEx(&cfg, balance_kernel<L, NV, true>, static_cast<const Args>(a));
+  else cudaLaunchKernelEx(&cfg, balance_kernel<L, NV, false>, static_cast<const Args>(a));
   return check_launch("balance_kernel");
 }
 
 nvfp4_status_t pass(Args& a, bool early, cudaStream_t s) {
   const bool vec = a.E % 4 == 0 && a.ld % 4 == 0 && aligned16(a.logits) && aligned16(a.dlogits);
-  switch (lanes_for(a.E)) {
-    case 2: return launch_pass<2>(a, vec, early, s);
-    case 4: return launch_pass<4>(a, vec, early, s);
-    case 8: return launch_pass<8>(a, vec, early, s);
-    case 16: return launch_pass<16>(a, vec, early, s);
-    default: return launch_pass<32>(a, vec, early, s);
+  const int L = lanes_for(a.E), nv = (a.E + 4 * L - 1) / (4 * L);  // nv >= 3 for L > 2
+  switch (L) {
+    case 2:
+      return nv == 1   ? launch_pass<2, 1>(a, vec, early, s)
+             : nv == 2 ? launch_pass<2, 2>(a, vec, early, s)
+             : nv == 3 ? launch_pass<2, 3>(a, vec, early, s)
+                       : launch_pass<2, 4>(a, vec, early, s);
+    case 4: return nv == 3 ? launch_pass<4, 3>(a, vec, early, s) : launch_pass<4, 4>(a, vec, early, s);
+    case 8: return nv == 3 ? launch_pass<8, 3>(a, vec, early, s) : launch_pass<8, 4>(a, vec, early, s);
+    default:
+      return nv == 3 ? launch_pass<16, 3>(a, vec, early, s) : launch_pass<16, 4>(a, vec, early, s);
   }
 }
 
