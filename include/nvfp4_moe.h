@@ -606,6 +606,56 @@ NVFP4_API nvfp4_status_t moe_balance_loss_backward(const float* logits, int64_t 
                                                    int accumulate, nvfp4_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------------
+ * nvfp4_residual_norm — the norms around a block: RMSNorm of its output, its gate, the scaled
+ * residual sum, and the RMSNorm in front of the next block, in one pass.
+ * nvfp4_residual_norm_backward — the gradients of all of it.
+ *
+ *   rstd(v) = 1 / sqrt(mean(v^2) + eps)
+ *   z  = y * rstd(y) * post_gamma        (z = y when post_gamma is NULL)
+ *   r' = r + scale * gate * z            (r' = r when y is NULL: a plain pre-norm)
+ *   n  = r' * rstd(r') * pre_gamma       (from the unrounded r'; not made when pre_gamma is NULL)
+ *   everything inside in FP32, r' and n each rounded once
+ *
+ *   r, r_out  [T][ld_r] and [T][H], r_dtype 0 = float32, 1 = bf16; r_out may be r (ld_r = H)
+ *   y         bf16 [T][ld_y] or NULL (then no post_gamma, no gate, and r_out is not written)
+ *   gate      bf16; gate_kind NVFP4_GATE_NONE (NULL: 1), _CHANNEL [H], _TOKEN [T] or _FULL [T][H]
+ *   post_gamma, pre_gamma  bf16 [H] or NULL
+ *   n_out     bf16 [T][H]
+ *   rstd_post, rstd_pre    float [T] or NULL: the rows' rstd(y) and rstd(r'), which the backward
+ *             call reads
+ *   Constraints: H % 8 == 0, H <= 16384, ld_r % 8 == 0, ld_y % 8 == 0, T < 2^31; bf16 and float
+ *   arrays 16-byte aligned (a token gate 2).
+ *
+ * Backward: the same inputs, and
+ *   dr_new, dn  gradients of r' [T][H] (of r's type) and of n (bf16 [T][H]); either may be NULL
+ *             (zero), not both
+ *   dr        [T][H] of r's type (may be dr_new); dy bf16 [T][H] (not written when y is NULL)
+ *   dpost_gamma, dpre_gamma  float [H] or NULL (not wanted)
+ *   dgate     float [H] (channel), float [T] (token) or bf16 [T][H] (full), or NULL
+ *   ws        device scratch of nvfp4_residual_norm_backward_workspace_size(T, H) bytes (needed
+ *             for the gradients of the gammas and of a channel gate)
+ *   Sums over rows are added in a fixed order (reproducible).
+ * ------------------------------------------------------------------------------------------- */
+#define NVFP4_GATE_NONE 0
+#define NVFP4_GATE_CHANNEL 1
+#define NVFP4_GATE_TOKEN 2
+#define NVFP4_GATE_FULL 3
+NVFP4_API nvfp4_status_t nvfp4_residual_norm(const void* r, int r_dtype, int64_t ld_r,
+                                             const void* y, int64_t ld_y, int64_t T, int H,
+                                             const void* post_gamma, const void* gate,
+                                             int gate_kind, float scale, const void* pre_gamma,
+                                             float eps, void* r_out, void* n_out,
+                                             float* rstd_post, float* rstd_pre,
+                                             nvfp4_stream_t stream);
+NVFP4_API size_t nvfp4_residual_norm_backward_workspace_size(int64_t T, int H);
+NVFP4_API nvfp4_status_t nvfp4_residual_norm_backward(
+    const void* dr_new, const void* dn, const void* r, int r_dtype, int64_t ld_r, const void* y,
+    int64_t ld_y, int64_t T, int H, const void* post_gamma, const void* gate, int gate_kind,
+    float scale, const void* pre_gamma, const float* rstd_post, const float* rstd_pre, void* dr,
+    void* dy, float* dpost_gamma, float* dpre_gamma, void* dgate, void* ws, size_t ws_bytes,
+    int32_t* dev_status, nvfp4_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
  * Status helpers.
  *   nvfp4_read_status: copies *dev_status to *host_code (host pointer) on `stream` and waits for
  *   the stream; returns NVFP4_ERR_TIMEOUT / NVFP4_ERR_BAD_INDEX when the matching bit is set.

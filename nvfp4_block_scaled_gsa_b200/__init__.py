@@ -35,6 +35,8 @@ from .api import (  # noqa: F401
     scale_from_amax,
     w1_row_map,
     read_status,
+    residual_norm,
+    residual_norm_backward,
     rows_max,
     sf_bytes,
     shared_expert,

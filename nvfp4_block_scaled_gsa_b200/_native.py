@@ -91,6 +91,14 @@ SIGNATURES = {
     "moe_balance_loss_backward": (c_int, [c_void, c_i64, c_int, c_int, c_int, c_void, c_void,
                                           c_void, c_int, c_void, c_float, c_void, c_void, c_int,
                                           c_void]),
+    "nvfp4_residual_norm": (c_int, [c_void, c_int, c_i64, c_void, c_i64, c_i64, c_int, c_void,
+                                    c_void, c_int, c_float, c_void, c_float, c_void, c_void,
+                                    c_void, c_void, c_void]),
+    "nvfp4_residual_norm_backward_workspace_size": (c_size, [c_i64, c_int]),
+    "nvfp4_residual_norm_backward": (c_int, [c_void, c_void, c_void, c_int, c_i64, c_void, c_i64,
+                                             c_i64, c_int, c_void, c_void, c_int, c_float, c_void,
+                                             c_void, c_void, c_void, c_void, c_void, c_void,
+                                             c_void, c_void, c_size, c_void, c_void]),
     "nvfp4_read_status": (c_int, [c_void, c_void, c_void]),
     "nvfp4_wait_selftest": (c_int, [c_i64, c_void, c_void, c_void]),
     "nvfp4_last_error": (c_char_p, []),

@@ -521,6 +521,95 @@ def balance_loss_backward(logits, counts, tokens, k, alpha, dloss=None, seq_offs
     return dlogits
 
 
+def _norm_operands(r, y, post_gamma, gate, pre_gamma):
+    """Checks shared by residual_norm and its gradient; returns (T, H, gate kind)."""
+    assert r.dtype in (BF16, F32) and r.dim() == 2 and r.stride(1) == 1
+    T, H = r.shape
+    _same_device(r.device, y, post_gamma, gate, pre_gamma)
+    if y is not None:
+        assert y.dtype == BF16 and y.shape == (T, H) and y.stride(1) == 1
+    for g in (post_gamma, pre_gamma):
+        assert g is None or (g.dtype == BF16 and g.shape == (H,) and g.is_contiguous())
+    kind = 0
+    if gate is not None:
+        assert gate.dtype == BF16 and gate.is_contiguous()
+        shape = tuple(gate.shape)
+        kind = (1 if shape == (H,) else 2 if shape in ((T,), (T, 1)) else
+                3 if shape == (T, H) else -1)
+        assert kind > 0, "gate must be (H,), (T,), (T, 1) or (T, H)"
+    return T, H, kind
+
+
+def residual_norm(r, y, post_gamma=None, gate=None, scale=1.0, pre_gamma=None, eps=1e-6,
+                  out_r=None, out_n=None):
+    """The norms around a block in one pass: z = RMSNorm(y) * post_gamma (z = y without one),
+    r' = r + scale * gate * z, n = RMSNorm(r') * pre_gamma.
+
+    r (T, H) bf16 or float32, y bf16 (T, H) (rows of both may be strided) or None (r' = r: a plain
+    pre-norm); gammas bf16 (H,); gate bf16, (H,) per channel, (T,) or (T, 1) per token, (T, H), or
+    None (a 1-D gate is per channel where T == H).  Returns (r', n, rstd of y (T,), rstd of r'
+    (T,)): r' in r's type (out_r may be r itself), n bf16 or None without pre_gamma, the last two
+    float32 (or None) for residual_norm_backward."""
+    T, H, kind = _norm_operands(r, y, post_gamma, gate, pre_gamma)
+    dev = r.device
+    _same_device(dev, out_r, out_n)
+    if y is None:
+        assert out_r is None
+        out_r = r
+    elif out_r is None:
+        out_r = torch.empty(T, H, dtype=r.dtype, device=dev)
+    assert out_r.dtype == r.dtype and out_r.shape == (T, H) and (y is None or out_r.is_contiguous())
+    rstd_post = rstd_pre = None
+    if post_gamma is not None:
+        rstd_post = torch.empty(T, dtype=F32, device=dev)
+    if pre_gamma is not None:
+        rstd_pre = torch.empty(T, dtype=F32, device=dev)
+        if out_n is None:
+            out_n = torch.empty(T, H, dtype=BF16, device=dev)
+        assert out_n.dtype == BF16 and out_n.shape == (T, H) and out_n.is_contiguous()
+    _call_on(dev, "nvfp4_residual_norm", _p(r), 0 if r.dtype == F32 else 1, _row_stride(r), _p(y),
+             H if y is None else _row_stride(y), T, H, _p(post_gamma), _p(gate), kind,
+             float(scale), _p(pre_gamma), float(eps), _p(out_r), _p(out_n), _p(rstd_post),
+             _p(rstd_pre))
+    return out_r, out_n, rstd_post, rstd_pre
+
+
+def residual_norm_backward(dr_new, dn, r, y, rstd_post, rstd_pre, post_gamma=None, gate=None,
+                           scale=1.0, pre_gamma=None, ws=None, status=None):
+    """The gradients of residual_norm from those of r' (dr_new, r's type) and n (dn, bf16), either
+    None for zero; the other arguments as given to and returned by residual_norm.  Returns a dict:
+    dr (r's type), dy (bf16), dpost_gamma and dpre_gamma (float32 (H,)), dgate (in the gate's
+    shape: float32 per channel or token, bf16 (T, H)); None where there is no such input."""
+    T, H, kind = _norm_operands(r, y, post_gamma, gate, pre_gamma)
+    dev = r.device
+    _same_device(dev, dr_new, dn, rstd_post, rstd_pre, ws, status)
+    if dr_new is not None:
+        assert dr_new.dtype == r.dtype and dr_new.shape == (T, H) and dr_new.is_contiguous()
+    if dn is not None:
+        assert dn.dtype == BF16 and dn.shape == (T, H) and dn.is_contiguous()
+    for v in (rstd_post, rstd_pre):
+        assert v is None or (v.dtype == F32 and v.shape == (T,) and v.is_contiguous())
+    dr = torch.empty(T, H, dtype=r.dtype, device=dev)
+    dy = dpost = dpre = dgate = None
+    if y is not None:
+        dy = torch.empty(T, H, dtype=BF16, device=dev)
+    if post_gamma is not None:
+        dpost = torch.empty(H, dtype=F32, device=dev)
+    if pre_gamma is not None:
+        dpre = torch.empty(H, dtype=F32, device=dev)
+    if kind:
+        dgate = torch.empty(gate.shape, dtype=BF16 if kind == 3 else F32, device=dev)
+    if ws is None:
+        ws = torch.empty(int(lib().nvfp4_residual_norm_backward_workspace_size(T, H)), dtype=U8,
+                         device=dev)
+    _call_on(dev, "nvfp4_residual_norm_backward", _p(dr_new), _p(dn), _p(r),
+             0 if r.dtype == F32 else 1, _row_stride(r), _p(y), H if y is None else _row_stride(y),
+             T, H, _p(post_gamma), _p(gate), kind, float(scale), _p(pre_gamma), _p(rstd_post),
+             _p(rstd_pre), _p(dr), _p(dy), _p(dpost), _p(dpre), _p(dgate), _p(ws), _bytes(ws),
+             _p(status))
+    return dict(dr=dr, dy=dy, dpost_gamma=dpost, dpre_gamma=dpre, dgate=dgate)
+
+
 def read_status(status):
     """Host copy of a device status word (synchronizes the current stream)."""
     host = torch.zeros(1, dtype=torch.int32)
