@@ -452,7 +452,7 @@ nvfp4_status_t check_common(const Args& a, int r_dtype) {
   if (a.T > INT32_MAX || a.H % 8 || a.H > kMaxH) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   if (a.ld_r < a.H || (a.y != nullptr && a.ld_y < a.H)) return NVFP4_ERR_INVALID_ARG;
   if (a.ld_r % 8 || (a.y != nullptr && a.ld_y % 8)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
-  if (a.y == nullptr && (a.post_gamma != nullptr || a.gate_kind != GATE_NONE))
+  if (a.T > 0 && a.y == nullptr && (a.post_gamma != nullptr || a.gate_kind != GATE_NONE))
     return NVFP4_ERR_INVALID_ARG;  // a post-norm or a gate of nothing
   if ((a.gate_kind != GATE_NONE) != (a.gate != nullptr)) return NVFP4_ERR_INVALID_ARG;
   const void* p16[] = {a.r, a.y, a.post_gamma, a.pre_gamma, a.r_out, a.n_out, a.dr_new, a.dn,
@@ -487,14 +487,15 @@ nvfp4_status_t launch_backward(const Args& a, cudaStream_t s) {
   const int threads = bwd_threads(a.H), ctas = bwd_ctas(a.T, a.H);
   const int per_sm = threads >= 512 ? 1 : 512 / threads;
   const int row = row_layout<F32>(a).bytes;
-  // a CTA's share of an SM's 228 KB, less its static shared memory and what the system reserves
-  const int room = 228 * 1024 / per_sm - 2560;
-  int stages = room / (row > 0 ? row : 1);
-  stages = stages < 1 ? 1 : stages > kBwdStages ? kBwdStages : stages;
-  const int smem = stages * row;
   // the largest row: float32 r and dr', a full gate, kMaxH columns
   constexpr int kMost = kMaxH * 14;
   static_assert(kMost + 2560 <= 228 * 1024, "one row of the widest form");
+  // a CTA's share of an SM's 228 KB, less its static shared memory and what the system reserves
+  int room = 228 * 1024 / per_sm - 2560;
+  room = room < kMost ? room : kMost;
+  int stages = room / (row > 0 ? row : 1);
+  stages = stages < 1 ? 1 : stages > kBwdStages ? kBwdStages : stages;
+  const int smem = stages * row;
   static std::atomic<uint64_t> devices_set{0};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -583,8 +584,8 @@ extern "C" nvfp4_status_t nvfp4_residual_norm_backward(
   nvfp4_status_t st = check_common(a, r_dtype);
   if (st != NVFP4_OK) return st;
   if (a.dn && !a.pre_gamma) return NVFP4_ERR_INVALID_ARG;
-  if (!dr_new && !dn) return NVFP4_ERR_INVALID_ARG;  // no gradient comes in
   if (T > 0) {
+    if (!dr_new && !dn) return NVFP4_ERR_INVALID_ARG;  // no gradient comes in
     if (!dr || (y && !dy)) return NVFP4_ERR_INVALID_ARG;
     if (dn && (!r || !rstd_pre)) return NVFP4_ERR_INVALID_ARG;
     if (y && post_gamma && !rstd_post) return NVFP4_ERR_INVALID_ARG;

@@ -1,0 +1,228 @@
+"""Host-side checks of the operators around the expert FFN (CPU only): workspace sizes, and every
+refusal before anything is launched."""
+
+import ctypes
+
+import pytest
+import torch
+
+import nvfp4_block_scaled_gsa_b200 as nv
+from nvfp4_block_scaled_gsa_b200 import build as B
+from nvfp4_block_scaled_gsa_b200 import _native as N
+
+F = ctypes.c_void_p(1 << 20)         # never dereferenced: every call below fails host validation
+ODD = ctypes.c_void_p((1 << 20) + 8)  # 4- but not 16-byte aligned
+BAD4 = ctypes.c_void_p((1 << 20) + 2)
+BIG = 1 << 40
+
+
+@pytest.fixture(scope="module")
+def L():
+    B.build()
+    return N.lib()
+
+
+def test_linear_w4a16_workspace(L):
+    ws = L.nvfp4_linear_w4a16_workspace_size
+    assert ws(1, 4096, 7168) == 0                       # a few rows: none
+    # 16 rows of 28 steps of 512 bytes and one word per row, in 256-byte units
+    assert ws(16, 4096, 7168) == 16 * 28 * 512 + 256
+    assert ws(100, 64, 64) == 100 * 512 + 512           # K rounded up to a whole step
+    assert ws(0, 64, 64) == 0 and ws(-1, 64, 64) == 0 and ws(4, 0, 64) == 0
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(K=100, ld=128), 2),            # K % 64
+    (dict(ld=64), 1),                    # ld < K
+    (dict(ld=132), 2),                   # ld % 8
+    (dict(M=-1), 1),
+    (dict(M=32 * 65535 + 1), 2),
+    (dict(N=0), 1),
+    (dict(out_dtype=2), 1),
+    (dict(x=None), 1),
+    (dict(w=None), 1),
+    (dict(sf=None), 1),
+    (dict(gs=None), 1),
+    (dict(out=None), 1),
+    (dict(x=ODD), 3),
+    (dict(w=ODD), 3),
+    (dict(sf=ODD), 3),
+    (dict(out=ODD), 3),
+    (dict(ws=ODD), 3),
+    (dict(gs=BAD4), 3),
+    (dict(status=BAD4), 3),
+    (dict(ws=None), 4),
+    (dict(ws_bytes=16), 4),
+    (dict(M=0, x=None, out=None, ws=None, ws_bytes=0), 0),
+])
+def test_linear_w4a16_refusals(L, change, code):
+    a = dict(x=F, M=16, K=128, ld=128, w=F, sf=F, gs=F, N=256, out=F, out_dtype=1, ws=F,
+             ws_bytes=BIG, status=None, stream=None)
+    a.update(change)
+    assert L.nvfp4_linear_w4a16(*a.values()) == code
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(H=192), 2),                    # H % 128
+    (dict(I=96), 2),                     # I % 64
+    (dict(E=257), 2),
+    (dict(E=0), 2),
+    (dict(k=9), 2),                      # k > E
+    (dict(k=0), 2),
+    (dict(T=4096 // 2 + 1), 2),          # more slots than the form takes
+    (dict(T=-1), 2),
+    (dict(x=None), 1),
+    (dict(logits=None), 1),              # neither logits nor a routing
+    (dict(ids=F, w=F), 1),               # both
+    (dict(logits=None, ids=F), 1),       # half a routing
+    (dict(ws=None), 1),
+    (dict(ws_bytes=100), 4),
+    (dict(w1=ODD), 3),
+    (dict(sf2=ODD), 3),
+    (dict(out=ODD), 3),
+    (dict(logits=BAD4), 3),
+    (dict(ws=ctypes.c_void_p((1 << 20) + 64)), 3),
+    (dict(T=0, x=None, ws=None, out=None), 0),
+])
+def test_moe_ffn_w4a16_refusals(L, change, code):
+    a = dict(x=F, logits=F, ids=None, w=None, T=4, H=256, I=128, E=8, k=2, w1=F, sf1=F, gs1=F, w2=F,
+             sf2=F, gs2=F, out=F, ws=F, ws_bytes=BIG, status=None, stream=None)
+    a.update(change)
+    assert L.moe_ffn_w4a16(*a.values()) == code
+
+
+def test_moe_ffn_w4a16_workspace(L):
+    ws = L.moe_ffn_w4a16_workspace_size
+    S, H, I = 16 * 8, 7168, 2048
+    assert ws(16, H, I, 256, 8) >= S * (H * 4 + I * 4 + I * 2) + 16 * H * 2
+    assert ws(-1, H, I, 256, 8) == 0 and ws(0, H, I, 256, 8) > 0
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(E=257, ld=257), 2),
+    (dict(k=33, E=64, ld=64), 2),
+    (dict(k=9), 2),
+    (dict(k=0), 1),
+    (dict(T=-1), 1),
+    (dict(ld=7), 1),
+    (dict(S=0), 1),
+    (dict(S=2, offs=None), 1),           # several sequences need their offsets
+    (dict(T=1 << 30), 2),                # T * k
+    (dict(logits=None), 1),
+    (dict(ids=None), 1),
+    (dict(counts=None), 1),
+    (dict(tokens=None), 1),
+    (dict(loss=None), 1),
+    (dict(ws=None), 1),
+    (dict(ws_bytes=8), 4),
+    (dict(logits=BAD4), 3),
+    (dict(offs=BAD4), 3),
+    (dict(dlogits=BAD4), 3),
+    (dict(ws=ODD), 3),
+])
+def test_balance_loss_refusals(L, change, code):
+    a = dict(logits=F, ld=8, T=16, E=8, k=2, ids=F, offs=F, S=1, mask=None, alpha=0.01, counts=F,
+             tokens=F, loss=F, dloss=None, dlogits=None, acc=0, ws=F, ws_bytes=BIG, status=None,
+             stream=None)
+    a.update(change)
+    assert L.moe_balance_loss(*a.values()) == code
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(E=300, ld=300), 2),
+    (dict(ld=4), 1),
+    (dict(S=3, offs=None), 1),
+    (dict(counts=None), 1),
+    (dict(tokens=None), 1),
+    (dict(dlogits=None), 1),
+    (dict(dloss=BAD4), 3),
+    (dict(T=0, logits=None, dlogits=None), 0),
+])
+def test_balance_loss_backward_refusals(L, change, code):
+    a = dict(logits=F, ld=8, T=16, E=8, k=2, counts=F, tokens=F, offs=None, S=1, mask=None,
+             alpha=0.01, dloss=None, dlogits=F, acc=0, stream=None)
+    a.update(change)
+    assert L.moe_balance_loss_backward(*a.values()) == code
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(H=60, ld_r=64, ld_y=64), 2),             # H % 8
+    (dict(H=16392, ld_r=16392, ld_y=16392), 2),    # wider than the form takes
+    (dict(ld_r=56), 1),
+    (dict(ld_y=56), 1),
+    (dict(ld_r=68), 2),
+    (dict(ld_y=68), 2),
+    (dict(dtype=2), 1),
+    (dict(T=-1), 1),
+    (dict(kind=4), 1),
+    (dict(kind=1), 1),                             # a kind without a gate
+    (dict(gate=F), 1),                             # a gate without a kind
+    (dict(y=None), 1),                             # a post-norm of nothing
+    (dict(eps=-1.0), 1),
+    (dict(eps=float("nan")), 1),
+    (dict(r=None), 1),
+    (dict(r_out=None), 1),
+    (dict(n_out=None), 1),
+    (dict(r=ODD), 3),
+    (dict(y=ODD), 3),
+    (dict(post=ODD), 3),
+    (dict(n_out=ODD), 3),
+    (dict(gate=ODD, kind=1), 3),
+    (dict(gate=ctypes.c_void_p((1 << 20) + 1), kind=2), 3),
+    (dict(rs1=BAD4), 3),
+    (dict(T=0, r=None, r_out=None), 0),
+])
+def test_residual_norm_refusals(L, change, code):
+    a = dict(r=F, dtype=1, ld_r=64, y=F, ld_y=64, T=4, H=64, post=F, gate=None, kind=0, scale=1.0,
+             pre=F, eps=1e-6, r_out=F, n_out=F, rs1=F, rs2=F, stream=None)
+    a.update(change)
+    assert L.nvfp4_residual_norm(*a.values()) == code
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(H=60, ld_r=64, ld_y=64), 2),
+    (dict(dr_new=None, dn=None), 1),               # no gradient comes in
+    (dict(pre=None, dpre=None), 1),                # dn without a pre-norm
+    (dict(rs2=None), 1),
+    (dict(rs1=None), 1),
+    (dict(r=None), 1),
+    (dict(dr=None), 1),
+    (dict(dy=None), 1),
+    (dict(post=None), 1),                          # dpost_gamma without a post-norm
+    (dict(dgate=F), 1),                            # dgate without a gate
+    (dict(ws=None), 4),
+    (dict(ws_bytes=100), 4),
+    (dict(dr_new=ODD), 3),
+    (dict(dn=ODD), 3),
+    (dict(dr=ODD), 3),
+    (dict(ws=ODD), 3),
+    (dict(gate=F, kind=3, dgate=ODD), 3),
+    (dict(dpost=BAD4), 3),
+])
+def test_residual_norm_backward_refusals(L, change, code):
+    a = dict(dr_new=F, dn=F, r=F, dtype=1, ld_r=64, y=F, ld_y=64, T=4, H=64, post=F, gate=None,
+             kind=0, scale=1.0, pre=F, rs1=F, rs2=F, dr=F, dy=F, dpost=F, dpre=F, dgate=None, ws=F,
+             ws_bytes=BIG, status=None, stream=None)
+    a.update(change)
+    assert L.nvfp4_residual_norm_backward(*a.values()) == code
+
+
+def test_residual_norm_backward_workspace(L):
+    ws = L.nvfp4_residual_norm_backward_workspace_size
+    assert ws(8192, 7168) == 148 * 2 * 7168 * 4    # one CTA per SM, two column sums each
+    assert ws(5, 64) == 5 * 2 * 64 * 4
+    assert ws(0, 64) == 0 and ws(4, 60) == 0 and ws(4, 1 << 20) == 0
+
+
+def test_wrappers_refuse_tensors_off_the_gpu():
+    x = torch.zeros(2, 64, dtype=torch.bfloat16)
+    w = nv.NVFP4Weights(torch.zeros(8, 32, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8),
+                        torch.ones(1), 1, 8, 64)
+    with pytest.raises(AssertionError):
+        nv.linear_w4a16(x, w)
+    with pytest.raises(AssertionError):
+        nv.balance_loss(torch.zeros(2, 4), torch.zeros(2, 1, dtype=torch.int32), 0.1)
+    with pytest.raises(AssertionError):
+        nv.residual_norm(x, x)
+    with pytest.raises(AssertionError):
+        nv.residual_norm(x.half(), x)              # a type it does not take
