@@ -80,6 +80,56 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
+// Two float32 values.  (The packed f32x2 instructions were tried for the backward pass: 151 us
+// against 138 for these at 8191 x 7168.)
+struct F2 {
+  float x, y;
+  __device__ __forceinline__ F2() {}
+  __device__ __forceinline__ F2(float lo, float hi) : x(lo), y(hi) {}
+  __device__ __forceinline__ explicit F2(float both) : x(both), y(both) {}
+  __device__ __forceinline__ float2 get() const { return make_float2(x, y); }
+};
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) { return F2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)); }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) { return F2(a.x * b.x, a.y * b.y); }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) { return F2(a.x + b.x, a.y + b.y); }
+__device__ __forceinline__ void unpack8(const uint4& q, F2 (&v)[4]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = F2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint4 pack8(const F2 (&v)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = v[i].get();
+    const __nv_bfloat162 p = __floats2bfloat162_rn(f.x, f.y);
+    w[i] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <bool F32>
+__device__ __forceinline__ void load8(const void* p, F2 (&v)[4]) {
+  if constexpr (F32) {
+    const float4 a = static_cast<const float4*>(p)[0], b = static_cast<const float4*>(p)[1];
+    v[0] = F2(a.x, a.y);
+    v[1] = F2(a.z, a.w);
+    v[2] = F2(b.x, b.y);
+    v[3] = F2(b.z, b.w);
+  } else {
+    unpack8(*static_cast<const uint4*>(p), v);
+  }
+}
+template <bool F32>
+__device__ __forceinline__ void store8(void* p, const F2 (&v)[4]) {
+  if constexpr (F32) {
+    const float2 a = v[0].get(), b = v[1].get(), c = v[2].get(), d = v[3].get();
+    static_cast<float4*>(p)[0] = make_float4(a.x, a.y, b.x, b.y);
+    static_cast<float4*>(p)[1] = make_float4(c.x, c.y, d.x, d.y);
+  } else {
+    *static_cast<uint4*>(p) = pack8(v);
+  }
+}
 // 8 residual values (bf16 or float32) at element i of a row; plain accesses, r_out may be r
 template <bool F32>
 __device__ __forceinline__ void load8(const void* row, int64_t i, float (&v)[8]) {
@@ -238,14 +288,21 @@ __host__ __device__ inline RowLayout row_layout(const Args& A) {
   return L;
 }
 
-// CTA b takes rows b, b + CTAs, ...  MAXT: threads at most (it sets the registers per thread).
-template <bool F32, int MAXT>
-__global__ void __launch_bounds__(MAXT) residual_norm_backward_kernel(const Args A, int stages) {
+// CTA b takes rows b, b + CTAs, ...  MAXT: threads at most (it sets the registers per thread);
+// FULL: the gate has a value per element (otherwise it is a factor per row or per column).  ALL: dr',
+// dn and y are all there (training's usual call), so that nothing is tested per element.
+//
+// Per element, with the row's k0 = scale * rstd(y), g_t (a token gate, or 1) and the column's
+// w = post_gamma * (a channel gate, or 1):
+//   c = k0 y w (its gradient side of the gate left out), r' = r + g_t c, u = rstd dn pre_gamma,
+//   a0 = dr' + u; sums of u r', c a0, c r'; then a = a0 - k r', dy = g_t k0 w a - k' y.
+template <bool F32, int MAXT, bool FULL, bool ALL>
+__global__ void __launch_bounds__(MAXT, 1) residual_norm_backward_kernel(const Args A, int stages) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bar[kBwdStages];
   __shared__ volatile int abort_flag;
   __shared__ float s_sum[2][3][32];
-  const int tid = threadIdx.x, H = A.H;
+  const int tid = threadIdx.x, lane = tid & 31, H = A.H;
   const RowLayout L = row_layout<F32>(A);
   const int res = F32 ? 4 : 2;
   if (tid == 0) {
@@ -265,7 +322,7 @@ __global__ void __launch_bounds__(MAXT) residual_norm_backward_kernel(const Args
     }
     if (A.y != nullptr) {
       bulk_load(d + L.y, A.y + t * A.ld_y, H * 2, b);
-      if (A.gate_kind == GATE_FULL) bulk_load(d + L.gate, A.gate + t * H, H * 2, b);
+      if constexpr (FULL) bulk_load(d + L.gate, A.gate + t * H, H * 2, b);
     }
   };
   const int64_t step = gridDim.x;
@@ -273,112 +330,171 @@ __global__ void __launch_bounds__(MAXT) residual_norm_backward_kernel(const Args
     for (int i = 0; i < stages; ++i)
       if (blockIdx.x + i * step < A.T) fetch(blockIdx.x + i * step, i);
 
-  // this thread's columns of the gammas and a channel gate
-  uint4 wpost[kBwdChunks], wpre[kBwdChunks], wgate[kBwdChunks];
+  // this thread's columns: their factors, and their sums over the rows of a * yhat (times scale
+  // and the gate, unless that is one per channel) and of dn * rhat
+  F2 w[kBwdChunks][4], acc_post[kBwdChunks][4], acc_pre[kBwdChunks][4];
+  uint4 wpre[kBwdChunks];
+  int cols[kBwdChunks];  // first column, or -1
 #pragma unroll
   for (int j = 0; j < kBwdChunks; ++j) {
     const int c = (tid + j * blockDim.x) * 8;
-    wpost[j] = wpre[j] = wgate[j] = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
-    if (c < H) {
-      if (A.post_gamma != nullptr) wpost[j] = __ldg(reinterpret_cast<const uint4*>(A.post_gamma + c));
-      if (A.pre_gamma != nullptr) wpre[j] = __ldg(reinterpret_cast<const uint4*>(A.pre_gamma + c));
-      if (A.gate_kind == GATE_CHANNEL) wgate[j] = __ldg(reinterpret_cast<const uint4*>(A.gate + c));
+    cols[j] = c < H ? c : -1;
+    wpre[j] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[j][i] = F2(1.0f);
+      acc_post[j][i] = acc_pre[j][i] = F2(0.0f);
     }
+    if (c >= H) continue;
+    if (A.post_gamma != nullptr)
+      unpack8(__ldg(reinterpret_cast<const uint4*>(A.post_gamma + c)), w[j]);
+    if (A.gate_kind == GATE_CHANNEL) {
+      F2 g[4];
+      unpack8(__ldg(reinterpret_cast<const uint4*>(A.gate + c)), g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[j][i] = mul2(w[j][i], g[i]);
+    }
+    if (A.pre_gamma != nullptr) wpre[j] = __ldg(reinterpret_cast<const uint4*>(A.pre_gamma + c));
   }
-  // sums over rows: of a * yhat (times the gate, unless that is one per channel) and dn * rhat
-  float acc_post[kBwdChunks][8], acc_pre[kBwdChunks][8];
-#pragma unroll
-  for (int j = 0; j < kBwdChunks; ++j)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc_post[j][i] = acc_pre[j][i] = 0.0f;
   const float inv_h = 1.0f / static_cast<float>(H);
-  const bool has_n = A.dn != nullptr, has_y = A.y != nullptr, post = A.post_gamma != nullptr;
+  const bool has_r = ALL || A.dr_new != nullptr, has_n = ALL || A.dn != nullptr;
+  const bool has_y = ALL || A.y != nullptr, post = A.post_gamma != nullptr;
 
-  int it = 0;
-  for (int64_t t = blockIdx.x; t < A.T; t += step, ++it) {
-    const int s = it % stages;
-    const float rs_y = has_y && post ? __ldg(A.rstd_post + t) : 1.0f;
-    const float rs_r = has_n ? __ldg(A.rstd_pre + t) : 0.0f;
-    const float g_tok = has_y && A.gate_kind == GATE_TOKEN ? __bfloat162float(A.gate[t]) : 1.0f;
-    const bool here = mbar_wait_bounded(smem_u32(&bar[s]), (it / stages) & 1, &abort_flag);
-    if (!__syncthreads_and(here)) break;  // all threads alike
+  // a row's scalars, read a row ahead
+  struct Scalars {
+    float rs_y, rs_r, g;
+  };
+  auto scalars = [&](int64_t t) {
+    Scalars v{1.0f, 0.0f, 1.0f};
+    if (t < A.T) {
+      if (has_y && post) v.rs_y = __ldg(A.rstd_post + t);
+      if (has_n) v.rs_r = __ldg(A.rstd_pre + t);
+      if (has_y && A.gate_kind == GATE_TOKEN) v.g = __bfloat162float(A.gate[t]);
+    }
+    return v;
+  };
+  Scalars next = scalars(blockIdx.x);
+  int it = 0, s = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+  char* dr_row = static_cast<char*>(A.dr) + (int64_t)blockIdx.x * H * res;
+  __nv_bfloat16* dy_row = A.dy + (int64_t)blockIdx.x * H;
+  for (int64_t t = blockIdx.x; t < A.T;
+       t += step, ++it, dr_row += step * H * res, dy_row += step * H) {
+    const float rs_y = next.rs_y, rs_r = next.rs_r, g_t = next.g;
+    next = scalars(t + step);
+    const float k0 = A.scale * rs_y;
+    ok = mbar_wait_bounded(smem_u32(&bar[s]), phase, &abort_flag);
     const uint8_t* row = smem + s * L.bytes;
-    float dr[kBwdChunks][8], rhat[kBwdChunks][8];
-    uint4 dnq[kBwdChunks], yq[kBwdChunks], gq[kBwdChunks];
-    float sums[3] = {0.0f, 0.0f, 0.0f};  // u * rhat, c * (dr' + rstd u), c * rhat (c without g_tok)
+    F2 a[kBwdChunks][4], rn[kBwdChunks][4];
+    uint4 yq[kBwdChunks], gq[kBwdChunks];
+    F2 sum2[3] = {F2(0.0f), F2(0.0f), F2(0.0f)};
+    const F2 k0_2(k0), g_2(g_t), rs_2(rs_r);
 #pragma unroll
     for (int j = 0; j < kBwdChunks; ++j) {
-      const int c = (tid + j * blockDim.x) * 8;
-      dnq[j] = yq[j] = make_uint4(0u, 0u, 0u, 0u);
-      gq[j] = wgate[j];
+      const int c = cols[j];
+      if (c < 0) continue;
+      uint4 dnq = make_uint4(0u, 0u, 0u, 0u);
+      yq[j] = gq[j] = dnq;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dr[j][i] = rhat[j][i] = 0.0f;
-      if (c >= H) continue;
-      if (A.dr_new != nullptr) load8<F32>(row, c, dr[j]);
+      for (int i = 0; i < 4; ++i) a[j][i] = rn[j][i] = F2(0.0f);
+      if (has_r) load8<F32>(row + c * res, a[j]);
+      if (has_n) {
+        load8<F32>(row + L.r + c * res, rn[j]);
+        dnq = *reinterpret_cast<const uint4*>(row + L.dn + c * 2);
+      }
       if (has_y) {
         yq[j] = *reinterpret_cast<const uint4*>(row + L.y + c * 2);
-        if (A.gate_kind == GATE_FULL) gq[j] = *reinterpret_cast<const uint4*>(row + L.gate + c * 2);
+        if constexpr (FULL) gq[j] = *reinterpret_cast<const uint4*>(row + L.gate + c * 2);
       }
-      float y[8], g[8], w[8], cc[8];
+      F2 y[4], dn[4], wp[4], g[4];
       unpack8(yq[j], y);
-      unpack8(gq[j], g);
-      unpack8(wpost[j], w);
+      unpack8(dnq, dn);
+      unpack8(wpre[j], wp);
+      if constexpr (FULL) unpack8(gq[j], g);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) cc[i] = A.scale * g[i] * w[i] * (y[i] * rs_y);
-      if (has_n) {
-        float rv[8], dn[8], wp[8];
-        load8<F32>(row + L.r, c, rv);
-        dnq[j] = *reinterpret_cast<const uint4*>(row + L.dn + c * 2);
-        unpack8(dnq[j], dn);
-        unpack8(wpre[j], wp);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          rhat[j][i] = (rv[i] + g_tok * cc[i]) * rs_r;
-          const float u = dn[i] * wp[i];
-          dr[j][i] += rs_r * u;
-          sums[0] += u * rhat[j][i];
-          sums[2] += cc[i] * rhat[j][i];
-          acc_pre[j][i] += dn[i] * rhat[j][i];
-        }
+      for (int i = 0; i < 4; ++i) {
+        F2 cc = mul2(mul2(y[i], k0_2), w[j][i]);
+        if constexpr (FULL) cc = mul2(cc, g[i]);
+        rn[j][i] = fma2(g_2, cc, rn[j][i]);
+        const F2 dnr = mul2(dn[i], rs_2), u = mul2(dnr, wp[i]);
+        a[j][i] = add2(a[j][i], u);
+        sum2[0] = fma2(u, rn[j][i], sum2[0]);
+        sum2[1] = fma2(cc, a[j][i], sum2[1]);
+        sum2[2] = fma2(cc, rn[j][i], sum2[2]);
+        acc_pre[j][i] = fma2(dnr, rn[j][i], acc_pre[j][i]);
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sums[1] += cc[i] * dr[j][i];
     }
-    cta_sums<3>(sums, s_sum[it & 1]);
-    if (blockDim.x <= 32) __syncwarp();
-    // every thread has read the stage (the barrier in cta_sums): on to a later row
+    float sums[3];
+#pragma unroll
+    for (int n = 0; n < 3; ++n) {
+      const float2 v = sum2[n].get();
+      sums[n] = v.x + v.y;
+    }
+    // the CTA's sums, in every thread; the barrier also tells that every thread has read the stage,
+    // and whether all found it filled
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int n = 0; n < 3; ++n) sums[n] += __shfl_xor_sync(0xffffffffu, sums[n], o);
+    if (blockDim.x > 32) {
+      if (lane == 0)
+#pragma unroll
+        for (int n = 0; n < 3; ++n) s_sum[it & 1][n][tid >> 5] = sums[n];
+      ok = __syncthreads_and(ok) != 0;
+#pragma unroll
+      for (int n = 0; n < 3; ++n)
+        sums[n] = lane < static_cast<int>(blockDim.x >> 5) ? s_sum[it & 1][n][lane] : 0.0f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int n = 0; n < 3; ++n) sums[n] += __shfl_xor_sync(0xffffffffu, sums[n], o);
+    } else {
+      ok = __all_sync(0xffffffffu, ok) != 0;
+    }
+    if (!ok) break;  // all threads alike
     if (tid == 0 && t + stages * step < A.T) fetch(t + stages * step, s);
-    const float k_r = rs_r * sums[0] * inv_h;         // a = dr' + rstd u - k_r * rhat
-    const float s_cy = sums[1] - k_r * sums[2];       // sum of c * a, without g_tok
-    const float k_y = post ? g_tok * s_cy * inv_h : 0.0f;  // mean of d * yhat
+    // mean(u rhat) rstd per r', and sum(c a) with a = a0 - k_r r'
+    const float k_r = sums[0] * inv_h * rs_r * rs_r;
+    const float s_ca = sums[1] - k_r * sums[2];
     if (tid == 0 && A.dgate != nullptr && A.gate_kind == GATE_TOKEN)
-      static_cast<float*>(A.dgate)[t] = s_cy;
+      static_cast<float*>(A.dgate)[t] = s_ca;
+    // mean(d yhat) yhat rstd(y) = g_t s_ca / H * rstd(y)^2 y
+    const F2 k1_2(g_t * k0), k_r2(-k_r), k_y2(post ? -g_t * s_ca * inv_h * rs_y * rs_y : 0.0f);
 #pragma unroll
     for (int j = 0; j < kBwdChunks; ++j) {
-      const int c = (tid + j * blockDim.x) * 8;
-      if (c >= H) continue;
-      float a[8];
+      const int c = cols[j];
+      if (c < 0) continue;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) a[i] = dr[j][i] - k_r * rhat[j][i];
-      store8<F32>(static_cast<char*>(A.dr) + t * H * res, c, a);
+      for (int i = 0; i < 4; ++i) a[j][i] = fma2(k_r2, rn[j][i], a[j][i]);
+      store8<F32>(dr_row + c * res, a[j]);
       if (!has_y) continue;
-      float y[8], g[8], w[8], dy[8], dg[8];
+      F2 y[4], dy[4], g[4], dg[4];
       unpack8(yq[j], y);
-      unpack8(gq[j], g);
-      unpack8(wpost[j], w);
+      if constexpr (FULL) unpack8(gq[j], g);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float yhat = y[i] * rs_y, sg = A.scale * g_tok * g[i];
-        dy[i] = rs_y * (sg * w[i] * a[i] - yhat * k_y);
-        dg[i] = A.scale * w[i] * yhat * a[i];
-        acc_post[j][i] += (A.gate_kind == GATE_CHANNEL ? 1.0f : g_tok * g[i]) * yhat * a[i];
+      for (int i = 0; i < 4; ++i) {
+        const F2 b = mul2(a[j][i], k1_2);
+        if constexpr (FULL) {
+          const F2 bw = mul2(b, w[j][i]);
+          dg[i] = mul2(bw, y[i]);
+          dy[i] = fma2(bw, g[i], mul2(k_y2, y[i]));
+          acc_post[j][i] = fma2(mul2(b, g[i]), y[i], acc_post[j][i]);
+        } else {
+          dy[i] = fma2(b, w[j][i], mul2(k_y2, y[i]));
+          acc_post[j][i] = fma2(b, y[i], acc_post[j][i]);
+        }
       }
-      *reinterpret_cast<uint4*>(A.dy + t * H + c) = pack8(dy);
-      if (A.gate_kind == GATE_FULL && A.dgate != nullptr)
+      *reinterpret_cast<uint4*>(dy_row + c) = pack8(dy);
+      if (FULL && A.dgate != nullptr)
         *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(A.dgate) + t * H + c) = pack8(dg);
     }
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1;
+    }
   }
-  if (abort_flag) {  // let the copies already issued land before the CTA can exit
+  if (!ok) {  // let the copies already issued land before the CTA can exit
     if (tid == 0) {
       report(A.status, NVFP4_DEVERR_TIMEOUT);
       volatile int never = 0;
@@ -394,10 +510,9 @@ __global__ void __launch_bounds__(MAXT) residual_norm_backward_kernel(const Args
   float* part = A.part + (int64_t)blockIdx.x * 2 * H;
 #pragma unroll
   for (int j = 0; j < kBwdChunks; ++j) {
-    const int c = (tid + j * blockDim.x) * 8;
-    if (c >= H) continue;
-    store8<true>(part, c, acc_post[j]);
-    store8<true>(part + H, c, acc_pre[j]);
+    if (cols[j] < 0) continue;
+    store8<true>(part + cols[j], acc_post[j]);
+    store8<true>(part + H + cols[j], acc_pre[j]);
   }
 }
 
@@ -426,8 +541,8 @@ __global__ void __launch_bounds__(256) norm_grads_kernel(const Args A, int parts
   const bool channel = A.gate_kind == GATE_CHANNEL;
   const float g = channel ? __bfloat162float(A.gate[col]) : 1.0f;
   const float w = A.post_gamma != nullptr ? __bfloat162float(A.post_gamma[col]) : 1.0f;
-  if (A.dpost_gamma != nullptr) A.dpost_gamma[col] = A.scale * g * v;
-  if (channel && A.dgate != nullptr) static_cast<float*>(A.dgate)[col] = A.scale * w * v;
+  if (A.dpost_gamma != nullptr) A.dpost_gamma[col] = g * v;
+  if (channel && A.dgate != nullptr) static_cast<float*>(A.dgate)[col] = w * v;
 }
 
 // ------------------------------------------------------------------------------ host side
@@ -481,9 +596,9 @@ void launch_forward(const Args& a, cudaStream_t s) {
   else residual_norm_kernel<F32, 1><<<grid, block, 0, s>>>(a);
 }
 
-template <bool F32, int MAXT>
+template <bool F32, int MAXT, bool FULL, bool ALL>
 nvfp4_status_t launch_backward(const Args& a, cudaStream_t s) {
-  auto* fn = residual_norm_backward_kernel<F32, MAXT>;
+  auto* fn = residual_norm_backward_kernel<F32, MAXT, FULL, ALL>;
   const int threads = bwd_threads(a.H), ctas = bwd_ctas(a.T, a.H);
   const int per_sm = threads >= 512 ? 1 : 512 / threads;
   const int row = row_layout<F32>(a).bytes;
@@ -507,6 +622,20 @@ nvfp4_status_t launch_backward(const Args& a, cudaStream_t s) {
   }
   fn<<<ctas, threads, smem, s>>>(a, stages);
   return check_launch("residual_norm_backward_kernel");
+}
+
+template <bool F32, bool FULL, bool ALL>
+nvfp4_status_t launch_backward(const Args& a, cudaStream_t s) {
+  return bwd_threads(a.H) <= 512 ? launch_backward<F32, 512, FULL, ALL>(a, s)
+                                 : launch_backward<F32, 1024, FULL, ALL>(a, s);
+}
+
+template <bool F32>
+nvfp4_status_t launch_backward(const Args& a, cudaStream_t s) {
+  const bool all = a.dr_new != nullptr && a.dn != nullptr && a.y != nullptr;
+  if (a.gate_kind == GATE_FULL)
+    return all ? launch_backward<F32, true, true>(a, s) : launch_backward<F32, true, false>(a, s);
+  return all ? launch_backward<F32, false, true>(a, s) : launch_backward<F32, false, false>(a, s);
 }
 
 }  // namespace
@@ -603,11 +732,7 @@ extern "C" nvfp4_status_t nvfp4_residual_norm_backward(
   int parts = 0;
   if (T > 0) {
     parts = bwd_ctas(T, H);
-    const bool few = bwd_threads(H) <= 512;
-    if (r_dtype == 0)
-      st = few ? launch_backward<true, 512>(a, s) : launch_backward<true, 1024>(a, s);
-    else
-      st = few ? launch_backward<false, 512>(a, s) : launch_backward<false, 1024>(a, s);
+    st = r_dtype == 0 ? launch_backward<true>(a, s) : launch_backward<false>(a, s);
     if (st != NVFP4_OK) return st;
   }
   if (!columns) return NVFP4_OK;
