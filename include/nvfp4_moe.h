@@ -518,7 +518,7 @@ NVFP4_API nvfp4_status_t moe_ffn_forward_ex(const void* x_bf16, const float* log
  *   by M, N and K (the result is reproducible).
  *   ws        device scratch of nvfp4_linear_w4a16_workspace_size(M, N, K) bytes (x in the order the
  *             product reads it, one word per row); 0 = none needed (a few rows), ws may be NULL
- *   Constraints: K % 64 == 0, any N >= 1, M <= 2,097,120.
+ *   Constraints: K % 64 == 0, any N >= 1, M <= 1,048,560.
  * ------------------------------------------------------------------------------------------- */
 NVFP4_API size_t nvfp4_linear_w4a16_workspace_size(int64_t M, int N, int K);
 NVFP4_API nvfp4_status_t nvfp4_linear_w4a16(const void* x, int64_t M, int K, int64_t ld,

@@ -28,33 +28,36 @@ __device__ __forceinline__ void topk_token(const float* __restrict__ logits, int
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
 
-  uint32_t taken = 0;
+  // Ordered keys: a larger float has a larger key, -0 and +0 the same one, a NaN none (0: it is
+  // never selected).  A round is two warp reductions: the largest key, then the lowest expert that
+  // has it.
+  uint32_t key[kPerLane];
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) {
+    const uint32_t b = __float_as_uint(v[i] + 0.0f);
+    key[i] = lane + 32 * i < E && v[i] == v[i] ? ((b >> 31) ? ~b : b | 0x80000000u) : 0u;
+  }
   int my_id = -1;
   float my_v = -INFINITY;
   for (int j = 0; j < k; ++j) {
-    float bv = -INFINITY;
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) best = max(best, key[i]);
+    best = __reduce_max_sync(0xffffffffu, best);
     int be = INT_MAX;
+    if (best != 0) {
 #pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
-      const int e = lane + 32 * i;
-      if (e < E && !((taken >> i) & 1u) && (v[i] > bv || (v[i] == bv && e < be))) {
-        bv = v[i];
-        be = e;
-      }
-    }
+      for (int i = kPerLane - 1; i >= 0; --i)
+        if (key[i] == best) be = lane + 32 * i;
+      be = static_cast<int>(__reduce_min_sync(0xffffffffu, static_cast<uint32_t>(be)));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
-      const int oe = __shfl_xor_sync(0xffffffffu, be, o);
-      if (ov > bv || (ov == bv && oe < be)) {
-        bv = ov;
-        be = oe;
-      }
+      for (int i = 0; i < kPerLane; ++i)
+        if (lane + 32 * i == be) key[i] = 0;
     }
-    if (be != INT_MAX && (be & 31) == lane) taken |= 1u << (be >> 5);
     if (lane == j) {
       my_id = be;
-      my_v = bv;
+      my_v = best == 0 ? -INFINITY
+                       : __uint_as_float((best >> 31) ? best ^ 0x80000000u : ~best);
     }
   }
   const bool live = lane < k && my_id != INT_MAX && my_v > -INFINITY && m > -INFINITY;

@@ -58,36 +58,22 @@ template <int NT, bool XIN>
 struct Cfg {
   static constexpr int TOK = 8 * NT;  // token columns
   static constexpr int STAGE = kWTile + kSTile + (XIN ? 0 : (TOK * kXRow + 1023) / 1024 * 1024);
-  // two CTAs per SM with up to 16 tokens (so that one's start and end overlap the other's
-  // stream), one with 32, whose accumulators need the registers
-  static constexpr int CTAS = NT == 4 ? 1 : 2;
-  static constexpr int STAGES = NT == 4 ? 6 : 4;
+  static constexpr int STAGES = 4;
   static constexpr int X_AT = STAGES * STAGE;  // XIN: the activations behind the stages
   static constexpr int SMEM = X_AT + (XIN ? kMaxPieces * kXRow : 0) + 1024;
   static_assert(kKWarps * TOK * kRedStride * 4 <= STAGES * STAGE, "partial sums reuse the stages");
   static_assert(STAGES % kKWarps == 0, "a stage is always the same K warps', or one could wait two phases ahead");
-  static_assert(CTAS * (SMEM + 3072) <= 227 * 1024, "shared memory of an SM");
+  // two CTAs per SM, so that one's start and end overlap the other's stream
+  static_assert(2 * (SMEM + 3072) <= 227 * 1024, "shared memory of an SM");
 };
 
-enum Mode { DENSE = 0, FFN_L1 = 1, FFN_L2 = 2 };
-
-struct Args {
+// A weight tensor and the converted activations it is multiplied with.
+struct Operands {
   const uint8_t* sf;      // per expert round_up(N, 128) rows of tiled scales
   const float* gs;        // [E]
   int N, K;
-  const void* x;          // XIN: bf16 activations, rows of ld_bytes
-  int64_t ld_bytes;
-  const uint8_t* xf;      // else: converted ones, [rows][steps][kStepX bytes]
-  const int32_t* exps;    // and [rows] the power of two each row was multiplied by
-  int M;                  // rows (DENSE)
-  int k;                  // slots per token (FFN)
-  const int4* plan;       // {expert, first, count, 0} per busy expert (FFN)
-  const int32_t* n_plan;  // number of busy experts
-  const int32_t* order;   // slots sorted by expert
-  void* out;              // DENSE: [M][N]; FFN_L1: float [slots][N/2]; FFN_L2: float [slots][N]
-  int out_f32;            // DENSE
-  int splits;             // CTAs of a cluster that share an output block along K
-  int32_t* status;
+  const uint8_t* xf;      // [rows][steps][kStepX bytes]
+  const int32_t* exps;    // [rows] the power of two each row was multiplied by
 };
 
 // Not volatile: pure functions of their operands, for the compiler to schedule.
@@ -168,69 +154,61 @@ __device__ __forceinline__ int32_t ld_after(const int32_t* p) {
   return v;
 }
 
-// 8 consecutive activations, as stored
-template <bool F32>
-struct X8 {
-  static constexpr int W = F32 ? 8 : 4;
-  uint32_t raw[W];
-  __device__ __forceinline__ void load(const void* row, int64_t k, bool ok) {
-#pragma unroll
-    for (int i = 0; i < W; i += 4) {
-      uint4 a = make_uint4(0u, 0u, 0u, 0u);
-      if (ok) a = ld_after16(static_cast<const uint8_t*>(row) + k * (W / 2) + i * 4);
-      raw[i] = a.x;
-      raw[i + 1] = a.y;
-      raw[i + 2] = a.z;
-      raw[i + 3] = a.w;
-    }
-  }
-  __device__ __forceinline__ float at(int i) const {
-    if constexpr (F32) return __uint_as_float(raw[i]);
-    else return __uint_as_float((i & 1) ? raw[i / 2] & 0xFFFF0000u : raw[i / 2] << 16);
-  }
-  // float32 bits of the largest finite magnitude
-  __device__ __forceinline__ uint32_t amax() const {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t b = __float_as_uint(at(i)) & 0x7FFFFFFFu;
-      if (b < 0x7F800000u) m = max(m, b);
-    }
-    return m;
-  }
-  // the 8 values times f, as f16
-  __device__ __forceinline__ uint4 to_f16(float f) const {
-    uint32_t h[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __half2 v = __floats2half2_rn(at(2 * i) * f, at(2 * i + 1) * f);
-      h[i] = *reinterpret_cast<const uint32_t*>(&v);
-    }
-    return make_uint4(h[0], h[1], h[2], h[3]);
-  }
-};
-
-// One CTA converts one row of K activations: the power of two, and the f16 values of every step of
-// 256 in the order [word of 8][quad lane] (zeros past K).  `red` holds a word per warp.
-constexpr int kPrepCache = 4;  // pieces of 8 a thread keeps between the two passes
-template <bool F32>
-__device__ __forceinline__ void convert_row(const void* row, int K, uint8_t* out, int32_t* exp_out,
-                                            uint32_t* red) {
-  const int tid = threadIdx.x, nthr = blockDim.x;
-  const int pieces = (K + kStepK - 1) / kStepK * (kStepK / 8);
-  X8<F32> c[kPrepCache];
+// float32 bits of the largest finite magnitude of some values
+template <int N>
+__device__ __forceinline__ uint32_t amax_of(const float (&v)[N]) {
   uint32_t m = 0;
 #pragma unroll
-  for (int j = 0; j < kPrepCache; ++j) {
-    const int64_t k = (int64_t)(tid + j * nthr) * 8;
-    c[j].load(row, k, k < K);
+  for (int i = 0; i < N; ++i) {
+    const uint32_t b = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+    if (b < 0x7F800000u) m = max(m, b);
   }
+  return m;
+}
+// the values times f, as f16, to `d`
+template <int N>
+__device__ __forceinline__ void put_f16(uint8_t* d, const float (&v)[N], float f) {
+  uint32_t h[N / 2];
 #pragma unroll
-  for (int j = 0; j < kPrepCache; ++j) m = max(m, c[j].amax());
-  for (int p = tid + kPrepCache * nthr; p < pieces; p += nthr) {
-    X8<F32> x;
-    x.load(row, (int64_t)p * 8, p * (int64_t)8 < K);
-    m = max(m, x.amax());
+  for (int i = 0; i < N / 2; ++i) {
+    const __half2 p = __floats2half2_rn(v[2 * i] * f, v[2 * i + 1] * f);
+    h[i] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  if constexpr (N == 8) *reinterpret_cast<uint4*>(d) = make_uint4(h[0], h[1], h[2], h[3]);
+  else *reinterpret_cast<uint2*>(d) = make_uint2(h[0], h[1]);
+}
+__device__ __forceinline__ void bf16x8(const uint4& q, float (&v)[8]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+// One CTA converts one row of K activations: the power of two, and the f16 values of every step of
+// 256 in the order [word of 8][quad lane] (zeros past K).  load(p, v) gives elements N*p .. N*p +
+// N-1, N = 4 or 8.  `red` holds a word per warp.
+template <int N, int kCache, typename Load>  // kCache: pieces a thread keeps between the two passes
+__device__ __forceinline__ void convert_row(const Load& load, int K, uint8_t* out, int32_t* exp_out,
+                                            uint32_t* red) {
+  const int tid = threadIdx.x, nthr = blockDim.x;
+  const int pieces = (K + kStepK - 1) / kStepK * (kStepK / N), live = K / N;
+  float c[kCache][N];
+  uint32_t m = 0;
+  auto get = [&](int p, float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = 0.0f;
+    if (p < live) load(p, v);
+  };
+#pragma unroll
+  for (int j = 0; j < kCache; ++j) get(tid + j * nthr, c[j]);
+#pragma unroll
+  for (int j = 0; j < kCache; ++j) m = max(m, amax_of(c[j]));
+  for (int p = tid + kCache * nthr; p < live; p += nthr) {
+    float v[N];
+    get(p, v);
+    m = max(m, amax_of(v));
   }
   m = __reduce_max_sync(0xffffffffu, m);
   if ((tid & 31) == 0) red[tid >> 5] = m;
@@ -239,75 +217,92 @@ __device__ __forceinline__ void convert_row(const void* row, int K, uint8_t* out
   const int e = norm_exp(m);
   const float f = pow2f(e);
   if (tid == 0) *exp_out = e;
-  // element 8p: step p / 32, quad lane (p % 32) / 8, word p % 8
-  auto put = [&](int p, const X8<F32>& x) {
-    *reinterpret_cast<uint4*>(out + (int64_t)(p >> 5) * kStepX +
-                              ((p & 7) * 4 + ((p >> 3) & 3)) * 16) = x.to_f16(f);
+  // element k: step k / 256, quad lane (k % 256) / 64, word (k % 64) / 8
+  auto put = [&](int p, const float (&v)[N]) {
+    const int k = p * N;
+    put_f16(out + (int64_t)(k >> 8) * kStepX + (((k >> 3) & 7) * 4 + ((k >> 6) & 3)) * 16 + (k & 7) * 2,
+            v, f);
   };
 #pragma unroll
-  for (int j = 0; j < kPrepCache; ++j)
+  for (int j = 0; j < kCache; ++j)
     if (tid + j * nthr < pieces) put(tid + j * nthr, c[j]);
-  for (int p = tid + kPrepCache * nthr; p < pieces; p += nthr) {
-    X8<F32> x;
-    x.load(row, (int64_t)p * 8, p * (int64_t)8 < K);
-    put(p, x);
+  for (int p = tid + kCache * nthr; p < pieces; p += nthr) {
+    float v[N];
+    get(p, v);
+    put(p, v);
   }
 }
+// ... of a bf16 row
+__device__ __forceinline__ void convert_bf16_row(const void* row, int K, uint8_t* out,
+                                                 int32_t* exp_out, uint32_t* red) {
+  convert_row<8, 4>([&](int p, float (&v)[8]) { bf16x8(__ldg(static_cast<const uint4*>(row) + p), v); },
+                    K, out, exp_out, red);
+}
 
-// One row per CTA.  F32: the FFN's intermediate (after its L1), else the caller's bf16 rows.
-template <bool F32>
-__global__ void __launch_bounds__(256) convert_kernel(const void* x, int64_t ld_bytes, int K,
+// One row of the caller's activations per CTA.
+__global__ void __launch_bounds__(256) convert_kernel(const uint8_t* x, int64_t ld_bytes, int K,
                                                       uint8_t* xf, int32_t* exps) {
   __shared__ uint32_t red[32];
   pdl_trigger();
-  if constexpr (F32) pdl_wait();
   const int64_t r = blockIdx.x, steps = (K + kStepK - 1) / kStepK;
-  convert_row<F32>(static_cast<const uint8_t*>(x) + r * ld_bytes, K, xf + r * steps * kStepX,
-                   exps + r, red);
+  convert_bf16_row(x + r * ld_bytes, K, xf + r * steps * kStepX, exps + r, red);
 }
 
 // The first kernel of the FFN.  CTA 0 makes the plan: top-k (with logits), slots counted per
-// expert, an exclusive scan, and the slots in place.  The order of an expert's slots is whatever
-// the atomics give; a slot's result does not depend on it (each is a column of its own).  The
-// other CTAs convert one token's activations each.
-__global__ void __launch_bounds__(512) plan_kernel(
-    const float* __restrict__ logits, int T, int E, int k, int32_t* ids, float* w,
+// expert, the experts cut into units of at most `tok` slots, and the slots in place, in ascending
+// order within an expert (each warp ranks a contiguous part of them).  The other CTAs convert one
+// token's activations each.
+constexpr int kPlanThreads = 512;
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(
+    const float* __restrict__ logits, int T, int E, int k, int tok, int32_t* ids, float* w,
     int4* __restrict__ plan, int32_t* __restrict__ n_plan, int32_t* __restrict__ order,
-    const void* __restrict__ x, int H, uint8_t* __restrict__ xf, int32_t* __restrict__ exps,
-    int32_t* __restrict__ dev_status) {
-  __shared__ int cnt[kMaxE];
-  __shared__ int cursor[kMaxE];
+    int32_t* __restrict__ slot_unit, const uint8_t* __restrict__ x, int H,
+    uint8_t* __restrict__ xf, int32_t* __restrict__ exps, int32_t* __restrict__ dev_status) {
+  constexpr int kWarps = kPlanThreads / 32;
+  __shared__ int hist[kWarps][kMaxE];
+  __shared__ int first_of[kMaxE], unit_of[kMaxE];
   __shared__ uint32_t red[32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
   if (blockIdx.x > 0) {
     const int64_t r = blockIdx.x - 1, steps = (H + kStepK - 1) / kStepK;
-    convert_row<false>(static_cast<const uint8_t*>(x) + r * H * 2, H, xf + r * steps * kStepX,
-                       exps + r, red);
+    convert_bf16_row(x + r * H * 2, H, xf + r * steps * kStepX, exps + r, red);
     return;
   }
-  if (tid < kMaxE) cnt[tid] = 0;
+  for (int i = tid; i < kWarps * kMaxE; i += kPlanThreads) (&hist[0][0])[i] = 0;
   if (logits != nullptr)
-    for (int t = warp; t < T; t += blockDim.x / 32) topk_token(logits, t, E, k, 1, lane, ids, w);
+    for (int t = warp; t < T; t += kWarps) topk_token(logits, t, E, k, 1, lane, ids, w);
   __syncthreads();  // also: this CTA's ids are visible to all its threads
-  const int S = T * k;
+  const int S = T * k, per = (S + kWarps - 1) / kWarps;
+  const int lo = min(S, warp * per), hi = min(S, lo + per);
   bool bad = false;
-  for (int s = tid; s < S; s += blockDim.x) {
+  for (int s = lo + lane; s < hi; s += 32) {
     const int e = ids[s];
     if (e >= E) bad = true;
-    else if (e >= 0) atomicAdd(&cnt[e], 1);
+    else if (e >= 0) atomicAdd(&hist[warp][e], 1);
   }
   if (bad) report(dev_status, NVFP4_DEVERR_BAD_INDEX);
   __syncthreads();
+  if (tid < kMaxE) {  // per expert: each warp's first rank, and the count
+    int run = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      const int c = hist[i][tid];
+      hist[i][tid] = run;
+      run += c;
+    }
+    first_of[tid] = run;
+  }
+  __syncthreads();
   if (warp == 0) {  // lane l: experts 8l..8l+7
-    int c[kPerLane], sum = 0, busy = 0;
+    int c[kPerLane], sum = 0, units = 0;
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) {
-      c[i] = cnt[lane * kPerLane + i];
+      c[i] = first_of[lane * kPerLane + i];
       sum += c[i];
-      busy += c[i] > 0;
+      units += (c[i] + tok - 1) / tok;
     }
-    int run = sum, at = busy;
+    int run = sum, at = units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, run, o);
@@ -319,319 +314,370 @@ __global__ void __launch_bounds__(512) plan_kernel(
     }
     if (lane == 31) *n_plan = at;
     run -= sum;
-    at -= busy;
+    at -= units;
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) {
-      cursor[lane * kPerLane + i] = run;
-      if (c[i] > 0) plan[at++] = make_int4(lane * kPerLane + i, run, c[i], 0);
+      const int e = lane * kPerLane + i;
+      first_of[e] = run;
+      unit_of[e] = at;
+      for (int j = 0; j < c[i]; j += tok)
+        plan[at++] = make_int4(e, run + j, min(tok, c[i] - j), 0);
       run += c[i];
     }
   }
   __syncthreads();
-  for (int s = tid; s < S; s += blockDim.x) {
-    const int e = ids[s];
-    if (e >= 0 && e < E) order[atomicAdd(&cursor[e], 1)] = s;
+  for (int base = lo; base < hi; base += 32) {
+    const int s = base + lane;
+    int e = s < hi ? ids[s] : -1;
+    if (e >= E) e = -1;
+    const unsigned peers = __match_any_sync(0xffffffffu, e);
+    const int before = __popc(peers & ((1u << lane) - 1u));
+    if (e >= 0) {
+      const int rank = hist[warp][e] + before;
+      order[first_of[e] + rank] = s;
+      slot_unit[s] = unit_of[e] + rank / tok;
+    } else if (s < hi) {
+      slot_unit[s] = -1;
+    }
+    __syncwarp();
+    if (e >= 0 && before == 0) hist[warp][e] += __popc(peers);
+    __syncwarp();
   }
 }
 
 // ------------------------------------------------------------------------- the product
 
-__device__ __forceinline__ void consumers_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory");
-}
-
-// XIN: the CTA converts the activations of its rows and its part of K itself, when they are few;
-// otherwise a kernel in front has converted them and they pass through the ring with the weights.
-template <int NT, Mode MODE, bool XIN>
-__global__ void __launch_bounds__(kThreads, Cfg<NT, XIN>::CTAS)
-    w4a16_kernel(const __grid_constant__ CUtensorMap tm, const Args A) {
-  static_assert(!XIN || MODE == DENSE, "the FFN's activations are converted in front");
-  using C = Cfg<NT, XIN>;
-  constexpr int TOK = C::TOK, STAGES = C::STAGES;
-  // Accumulators of one step: with one token tile each row pair has two, so that a warp's
-  // consecutive MMAs do not wait for one another.
-  constexpr int CH = NT == 1 ? 2 : 1;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ __align__(8) uint64_t bar_full[STAGES], bar_empty[STAGES];
-  __shared__ volatile int abort_flag;
-  __shared__ __align__(16) uint8_t zeros[kStepX];  // what columns without a token read
-  __shared__ int s_row[TOK], s_exp[TOK];           // output row and power of two of each column
-  __shared__ uint32_t s_amax[TOK];                 // XIN
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = lane >> 2, q = lane & 3;
-  const int split = static_cast<int>(blockIdx.x) % A.splits;
-  const int rowblk = static_cast<int>(blockIdx.x) / A.splits;
-  if (tid == 0) {
-    abort_flag = 0;
-    for (int i = 0; i < STAGES; ++i) {
-      mbar_init(smem_u32(&bar_full[i]), 1);
-      mbar_init(smem_u32(&bar_empty[i]), kRowWarps);
-    }
-    fence_mbar_init();
+// What a lane reads of a stage, and the products of one step: 8 words of 8 codes per row.  The sums
+// of a step start from zero and are added to the running sums in plain float32 (the MMA truncates
+// as it accumulates, and over a long K that would drift).
+template <int NT>
+struct Lane {
+  int code_off, piece[2], scale_off, q;
+  __device__ __forceinline__ Lane(int rg, int lane) {
+    const int g = lane >> 2;
+    q = lane & 3;
+    // two 16-byte pieces of a row's 128 bytes (128-byte swizzle: the piece index is xored with the
+    // row's index modulo 8, which is g for all of the lane's rows)
+    code_off = (8 * rg + g) * 128;
+    piece[0] = ((2 * q) ^ g) * 16;
+    piece[1] = ((2 * q + 1) ^ g) * 16;
+    scale_off = kWTile + q * 512 + (8 * rg + g) * 16;
   }
-  if (tid < kStepX / 16) reinterpret_cast<uint4*>(zeros)[tid] = make_uint4(0u, 0u, 0u, 0u);
-  __syncthreads();
-
-  // Which tokens, against which expert.  The L2 form's plan is older than the kernel it waits
-  // for (the conversion of the intermediate, itself behind the L1), so it is read before that
-  // wait and the first weights are already on their way during it.
-  int e = 0, first = 0, count = A.M;
-  if constexpr (MODE == FFN_L1) pdl_wait();
-  if constexpr (MODE != DENSE) {
-    pdl_trigger();
-    if (static_cast<int>(blockIdx.y) >= ld_after(A.n_plan)) {  // the whole cluster
-      pdl_wait();  // no kernel of the chain ends before the ones in front of it
-      return;
+  // left: elements of K from the step's first one on (the last step may hold fewer than 256)
+  __device__ __forceinline__ void step(const uint8_t* st, const uint8_t* const (&xb)[NT], int left,
+                                       float (&acc)[2][NT][4]) const {
+    // with one token tile each row pair has two accumulators, so that a warp's consecutive MMAs do
+    // not wait for one another
+    constexpr int CH = NT == 1 ? 2 : 1;
+    uint32_t sc[4][2];
+    {
+      uint4 sv = lds16(st + scale_off);
+      // past K the codes are zeros, but the scale bytes are whatever was there
+      if (q * 64 >= left) sv = make_uint4(0u, 0u, 0u, 0u);
+      const uint32_t sw[4] = {sv.x, sv.y, sv.z, sv.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sc[j][0] = decode_scales(sw[j] & 0xFFFFu);
+        sc[j][1] = decode_scales(sw[j] >> 16);
+      }
     }
-    const uint4 p = ld_after16(A.plan + blockIdx.y);
-    e = static_cast<int>(p.x);
-    first = static_cast<int>(p.y);
-    count = static_cast<int>(p.z);
-  }
-  const int atoms_k = A.K / 64;
-  const int64_t blk_rows = (A.N + 127) / 128;
-  const uint8_t* sf = A.sf + ((int64_t)e * blk_rows + rowblk) * atoms_k * 512;
-  const uint32_t gs_bits = __float_as_uint(__ldg(A.gs + e));  // a positive normal number
-  const int gs_exp = static_cast<int>(gs_bits >> 23) - 127;
-  const float gs_frac = __uint_as_float((gs_bits & 0x7FFFFFu) | 0x3F800000u);
-  const int nsteps = (A.K + kStepK - 1) / kStepK;
-  const int st0 = static_cast<int>((int64_t)nsteps * split / A.splits);
-  const int n_st = static_cast<int>((int64_t)nsteps * (split + 1) / A.splits) - st0;
-
-  // token blocks of TOK: the dense form takes them from the grid, the FFN (an expert rarely has
-  // more than one) in a loop
-  const int tb_first = MODE == DENSE ? static_cast<int>(blockIdx.y) : 0;
-  const int tb_last = MODE == DENSE ? tb_first + 1 : (count + TOK - 1) / TOK;
-  uint32_t it0 = 0;  // stages used by earlier token blocks
-  for (int tb = tb_first; tb < tb_last; ++tb, it0 += n_st) {
-    const int ntok = min(TOK, count - tb * TOK);
-    auto out_row = [&](int t) {  // DENSE: the row of x; FFN: the slot
-      return MODE == DENSE ? tb * TOK + t : ld_after(A.order + first + tb * TOK + t);
-    };
-    auto x_row = [&](int r) { return MODE == FFN_L1 ? r / A.k : r; };
-    float acc[2][NT][4];
+    float tmp[CH][2][NT][4];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint32_t w[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint4 v = lds16(st + code_off + j * (32 * 128) + piece[half]);
+        w[j][0] = v.x;
+        w[j][1] = v.y;
+        w[j][2] = v.z;
+        w[j][3] = v.w;
+      }
+#pragma unroll
+      for (int wd = 0; wd < 4; ++wd) {
+        uint4 b[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) b[n] = lds16(xb[n] + half * 256 + wd * 64);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          uint32_t a[2][4];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            decode8(w[2 * p + r][wd], a[r]);
+            // the scale of 16-element group 2 * half + wd / 2, in both halves
+            const uint32_t sv =
+                __byte_perm(sc[2 * p + r][half], 0u, (wd & 2) ? 0x3232u : 0x1010u);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) a[r][j] = mul_f16x2(a[r][j], sv);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            auto& t0 = tmp[0][p][n];
+            auto& t1 = tmp[CH - 1][p][n];
+            if (half == 0 && wd == 0) {
+              mma_f16_first(t0, a[0][0], a[1][0], a[0][1], a[1][1], b[n].x, b[n].y);
+              if constexpr (CH == 2)
+                mma_f16_first(t1, a[0][2], a[1][2], a[0][3], a[1][3], b[n].z, b[n].w);
+              else
+                mma_f16(t1, a[0][2], a[1][2], a[0][3], a[1][3], b[n].z, b[n].w);
+            } else {
+              mma_f16(t0, a[0][0], a[1][0], a[0][1], a[1][1], b[n].x, b[n].y);
+              mma_f16(t1, a[0][2], a[1][2], a[0][3], a[1][3], b[n].z, b[n].w);
+            }
+          }
+        }
+      }
+    }
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[p][n][j] = 0.0f;
+        for (int j = 0; j < 4; ++j) {
+          acc[p][n][j] += tmp[0][p][n][j];
+          if (CH == 2) acc[p][n][j] += tmp[CH - 1][p][n][j];
+        }
+  }
+};
 
-    if (warp == kConsumers) {
-      // =========================== copies ===========================
-      const int64_t wrow = (int64_t)e * A.N + rowblk * 128;
-      bool ok = true;
-      auto wait_empty = [&](int i) {
-        const uint32_t it = it0 + i;
-        const bool mine =
-            mbar_wait_bounded(smem_u32(&bar_empty[it % STAGES]), ((it / STAGES) & 1u) ^ 1u, &abort_flag);
-        return __all_sync(0xffffffffu, mine) != 0;
-      };
-      auto copy_w = [&](int i) {  // codes and scales of step st0 + i
-        const uint32_t s = (it0 + i) % STAGES;
-        if (lane == 0) {
-          const int st = st0 + i, atoms = min(4, atoms_k - st * 4);
-          const uint32_t bar = smem_u32(&bar_full[s]), d = smem_u32(smem + s * C::STAGE);
-          mbar_arrive_expect_tx(bar, kWTile + atoms * 512 + (XIN ? 0 : ntok * kStepX));
-          tma_load_2d(d, &tm, bar, st * 128, static_cast<int>(wrow));
-          bulk_load(d + kWTile, sf + (int64_t)st * 4 * 512, atoms * 512, bar);
-        }
-        __syncwarp();
-      };
-      const uint8_t* xr = nullptr;
-      auto copy_x = [&](int i) {  // lane t: token t
-        const uint32_t s = (it0 + i) % STAGES;
-        if (!XIN && lane < ntok)
-          bulk_load(smem_u32(smem + s * C::STAGE + kWTile + kSTile) + lane * kXRow,
-                    xr + (int64_t)(st0 + i) * kStepX, kStepX, smem_u32(&bar_full[s]));
-      };
-      const int head = min(n_st, STAGES);
-      int issued = 0;
-      for (; issued < head && ok; ++issued) {
-        ok = wait_empty(issued);
-        if (!ok) break;
-        copy_w(issued);
+template <int NT>
+__device__ __forceinline__ void clear(float (&acc)[2][NT][4]) {
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[p][n][j] = 0.0f;
+}
+
+// The global scale (a positive normal number) as 2^exp * frac, and a sum times 2^-row_exp / 2^exp in
+// two exact steps; dividing by frac is left.
+struct GlobalScale {
+  int exp;
+  float frac;
+  __device__ __forceinline__ explicit GlobalScale(float gs) {
+    const uint32_t b = __float_as_uint(gs);
+    exp = static_cast<int>(b >> 23) - 127;
+    frac = __uint_as_float((b & 0x7FFFFFu) | 0x3F800000u);
+  }
+  __device__ __forceinline__ void factors(int row_exp, float& f0, float& f1) const {
+    const int up = -row_exp - exp;  // within [-253, 240]
+    f0 = pow2f(up / 2);
+    f1 = pow2f(up - up / 2);
+  }
+};
+
+// The stage ring: the barriers, and the copies of a step's codes and scales.
+template <int STAGES>
+struct Ring {
+  uint64_t *full, *empty;
+  volatile int* abort_flag;
+  __device__ __forceinline__ void init() const {  // by one thread
+    *abort_flag = 0;
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&empty[i]), kRowWarps);
+    }
+    fence_mbar_init();
+  }
+  // whole-warp waits: every lane gets the same answer
+  __device__ __forceinline__ bool wait_empty(uint32_t it) const {
+    const bool mine =
+        mbar_wait_bounded(smem_u32(&empty[it % STAGES]), ((it / STAGES) & 1u) ^ 1u, abort_flag);
+    return __all_sync(0xffffffffu, mine) != 0;
+  }
+  __device__ __forceinline__ bool wait_full(uint32_t it) const {
+    const bool mine =
+        mbar_wait_bounded(smem_u32(&full[it % STAGES]), (it / STAGES) & 1u, abort_flag);
+    return __all_sync(0xffffffffu, mine) != 0;
+  }
+  __device__ __forceinline__ void release(uint32_t it) const {  // by a warp of the step
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&empty[it % STAGES]));
+  }
+  // by the copying warp: step st of the 128 rows from `row` on, whose scale atoms start at `sf`;
+  // x_bytes of activations follow
+  __device__ __forceinline__ void copy_w(uint32_t it, uint8_t* stage, const CUtensorMap* tm, int row,
+                                         const uint8_t* sf, int st, int atoms_k, int x_bytes) const {
+    if ((threadIdx.x & 31) == 0) {
+      const int atoms = min(4, atoms_k - st * 4);
+      const uint32_t bar = smem_u32(&full[it % STAGES]), d = smem_u32(stage);
+      mbar_arrive_expect_tx(bar, kWTile + atoms * 512 + x_bytes);
+      tma_load_2d(d, tm, bar, st * 128, row);
+      bulk_load(d + kWTile, sf + (int64_t)st * 4 * 512, atoms * 512, bar);
+    }
+    __syncwarp();
+  }
+  // by lane t: token t's activations of a step
+  __device__ __forceinline__ void copy_x(uint32_t it, uint8_t* stage, const uint8_t* x) const {
+    bulk_load(smem_u32(stage) + kWTile + kSTile + (threadIdx.x & 31) * kXRow, x, kStepX,
+              smem_u32(&full[it % STAGES]));
+  }
+  // after a wait ran out: let the copies already issued land before the CTA can exit
+  __device__ __forceinline__ void drain(uint32_t issued) const {
+    volatile int never = 0;
+    for (uint32_t i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
+      mbar_wait_bounded(smem_u32(&full[i % STAGES]), (i / STAGES) & 1u, &never,
+                        NVFP4_WAIT_TIMEOUT_NS / 4);
+  }
+};
+
+__device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
+  return p + ((1024u - (smem_u32(p) & 1023u)) & 1023u);
+}
+__device__ __forceinline__ void consumers_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory");
+}
+
+// --------------------------------------------------------------- dense, one output block a cluster
+
+struct DenseArgs {
+  const void* x;  // XIN: bf16 activations, rows of ld_bytes
+  int64_t ld_bytes;
+  int M;
+  void* out;  // [M][N]
+  int out_f32;
+  int splits;  // CTAs of a cluster that share an output block along K
+  int32_t* status;
+};
+
+// For few output blocks: 128 rows of the weight and up to 8 * NT rows of x per cluster, K cut among
+// its CTAs, whose sums are joined through distributed shared memory.  XIN: the CTA converts the
+// activations of its rows and its part of K itself, when they are few; otherwise a kernel in
+// front has converted them and they pass through the ring with the weights.
+template <int NT, bool XIN>
+__global__ void __launch_bounds__(kThreads, 2)
+    dense_kernel(const __grid_constant__ CUtensorMap tm, const Operands W, const DenseArgs A) {
+  using C = Cfg<NT, XIN>;
+  constexpr int TOK = C::TOK, STAGES = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  __shared__ __align__(8) uint64_t bar_full[STAGES], bar_empty[STAGES];
+  __shared__ volatile int abort_flag;
+  __shared__ __align__(16) uint8_t zeros[kStepX];  // what columns without a token read
+  __shared__ int s_exp[TOK];                       // power of two of each column
+  __shared__ uint32_t s_amax[TOK];                 // XIN
+  const Ring<STAGES> ring{bar_full, bar_empty, &abort_flag};
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, q = lane & 3;
+  const int split = static_cast<int>(blockIdx.x) % A.splits;
+  const int rowblk = static_cast<int>(blockIdx.x) / A.splits;
+  const int m0 = static_cast<int>(blockIdx.y) * TOK, ntok = min(TOK, A.M - m0);
+  if (tid == 0) ring.init();
+  if (tid < kStepX / 16) reinterpret_cast<uint4*>(zeros)[tid] = make_uint4(0u, 0u, 0u, 0u);
+  __syncthreads();
+  const int atoms_k = W.K / 64, nsteps = (W.K + kStepK - 1) / kStepK;
+  const int st0 = static_cast<int>((int64_t)nsteps * split / A.splits);
+  const int n_st = static_cast<int>((int64_t)nsteps * (split + 1) / A.splits) - st0;
+  const GlobalScale gs(__ldg(W.gs));
+  float acc[2][NT][4];
+  clear<NT>(acc);
+  if (warp == kConsumers) {
+    const uint8_t* sf = W.sf + (int64_t)rowblk * atoms_k * 512;
+    auto stage = [&](int i) { return smem + (i % STAGES) * C::STAGE; };
+    auto copy_w = [&](int i) {
+      ring.copy_w(i, stage(i), &tm, rowblk * 128, sf, st0 + i, atoms_k, XIN ? 0 : ntok * kStepX);
+    };
+    const uint8_t* xr = W.xf + ((int64_t)(m0 + lane) * nsteps + st0) * kStepX;
+    auto copy_x = [&](int i) {
+      if (!XIN && lane < ntok) ring.copy_x(i, stage(i), xr + (int64_t)i * kStepX);
+    };
+    bool ok = true;
+    int issued = 0;
+    for (; issued < min(n_st, STAGES); ++issued) copy_w(issued);  // while x is converted
+    pdl_wait();
+    for (int i = 0; i < issued; ++i) copy_x(i);
+    for (; issued < n_st && ok; ++issued) {
+      ok = ring.wait_empty(issued);
+      if (!ok) break;
+      copy_w(issued);
+      copy_x(issued);
+    }
+    if (!ok) ring.drain(issued);
+  } else {
+    const int rg = warp % kRowWarps, wk = warp / kRowWarps;
+    const Lane<NT> me(rg, lane);
+    if constexpr (XIN) {
+      // pieces (token, step) warp and warp + kConsumers: lane l holds elements 8l .. 8l + 7
+      const int pieces = ntok * n_st;
+      constexpr int kMine = kMaxPieces / kConsumers;
+      float c[kMine][8];
+#pragma unroll
+      for (int j = 0; j < kMine; ++j) {
+        const int p = warp + j * kConsumers, k = (st0 + p % n_st) * kStepK + lane * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[j][i] = 0.0f;
+        if (p < pieces && k < W.K)
+          bf16x8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(A.x) +
+                                                      (int64_t)(m0 + p / n_st) * A.ld_bytes + k * 2)),
+                 c[j]);
       }
-      // the activations come from the kernel before (and for the L1 and later token blocks this
-      // has been waited for already)
+      if (tid < TOK) s_amax[tid] = 0;
+      consumers_sync();
+#pragma unroll
+      for (int j = 0; j < kMine; ++j) {
+        const int p = warp + j * kConsumers;
+        if (p < pieces) {
+          const uint32_t m = __reduce_max_sync(0xffffffffu, amax_of(c[j]));
+          if (lane == 0) atomicMax(&s_amax[p / n_st], m);
+        }
+      }
+      consumers_sync();
+      if (tid < TOK) s_exp[tid] = norm_exp(s_amax[tid]);
+#pragma unroll
+      for (int j = 0; j < kMine; ++j) {
+        const int p = warp + j * kConsumers;
+        if (p < pieces)
+          put_f16(smem + C::X_AT + p * kXRow + ((lane & 7) * 4 + (lane >> 3)) * 16, c[j],
+                  pow2f(norm_exp(s_amax[p / n_st])));
+      }
+      consumers_sync();
+    } else if (tid < ntok) {
       pdl_wait();
-      if (!XIN && lane < ntok) xr = A.xf + (int64_t)x_row(out_row(lane)) * nsteps * kStepX;
-      for (int i = 0; i < issued; ++i) copy_x(i);
-      for (; issued < n_st && ok; ++issued) {
-        ok = wait_empty(issued);
-        if (!ok) break;
-        copy_w(issued);
-        copy_x(issued);
-      }
-      if (!ok) {  // let the copies already issued land before the CTA can exit
-        volatile int never = 0;
-        for (int i = max(0, issued - STAGES); i < issued; ++i)
-          mbar_wait_bounded(smem_u32(&bar_full[(it0 + i) % STAGES]), ((it0 + i) / STAGES) & 1u,
-                            &never, NVFP4_WAIT_TIMEOUT_NS / 4);
-      }
-    } else {
-      // =========================== products ===========================
-      if (tid < ntok) {
-        pdl_wait();
-        const int r = out_row(tid);
-        s_row[tid] = r;
-        if (!XIN) s_exp[tid] = ld_after(A.exps + x_row(r));
-      }
-      if constexpr (XIN) {
-        // pieces (token, step) warp and warp + kConsumers: lane l holds elements 8l .. 8l + 7
-        const int pieces = ntok * n_st;
-        X8<false> c[kMaxPieces / kConsumers];
+      s_exp[tid] = ld_after(W.exps + m0 + tid);
+    }
+    for (int i = wk; i < n_st; i += kKWarps) {
+      if (!ring.wait_full(i)) break;
+      const uint8_t* st = smem + (i % STAGES) * C::STAGE;
+      const uint8_t* xb[NT];
 #pragma unroll
-        for (int j = 0; j < kMaxPieces / kConsumers; ++j) {
-          const int p = warp + j * kConsumers, k = (st0 + p % n_st) * kStepK + lane * 8;
-          if (p < pieces)
-            c[j].load(static_cast<const uint8_t*>(A.x) + (int64_t)(tb * TOK + p / n_st) * A.ld_bytes,
-                      k, k < A.K);
-        }
-        if (tid < TOK) s_amax[tid] = 0;
-        consumers_sync();
+      for (int n = 0; n < NT; ++n)
+        xb[n] = (n * 8 + g >= ntok ? zeros
+                 : XIN ? smem + C::X_AT + ((n * 8 + g) * n_st + i) * kXRow
+                       : st + kWTile + kSTile + (n * 8 + g) * kXRow) +
+                q * 16;
+      me.step(st, xb, W.K - (st0 + i) * kStepK, acc);
+      ring.release(i);
+    }
+  }
+
+  // partial sums of the K warps and of the cluster's CTAs -> shared memory, added in order
+  __syncthreads();
+  float* red = reinterpret_cast<float*>(smem);  // [kKWarps][TOK][kRedStride]
+  if (warp < kConsumers) {
+    const int rg = warp % kRowWarps, wk = warp / kRowWarps;
 #pragma unroll
-        for (int j = 0; j < kMaxPieces / kConsumers; ++j) {
-          const int p = warp + j * kConsumers;
-          if (p < pieces) {
-            const uint32_t m = __reduce_max_sync(0xffffffffu, c[j].amax());
-            if (lane == 0) atomicMax(&s_amax[p / n_st], m);
-          }
-        }
-        consumers_sync();
-        if (tid < TOK) s_exp[tid] = norm_exp(s_amax[tid]);
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int j = 0; j < kMaxPieces / kConsumers; ++j) {
-          const int p = warp + j * kConsumers;
-          if (p < pieces)
-            *reinterpret_cast<uint4*>(smem + C::X_AT + p * kXRow +
-                                      ((lane & 7) * 4 + (lane >> 3)) * 16) =
-                c[j].to_f16(pow2f(norm_exp(s_amax[p / n_st])));
-        }
-        consumers_sync();
-      }
-      const int rg = warp % kRowWarps, wk = warp / kRowWarps;
-      // this lane's two 16-byte pieces of a row's 128 bytes (128-byte swizzle: the piece index is
-      // xored with the row's index modulo 8, which is g for all of the lane's rows)
-      const int row_off = (8 * rg + g) * 128;
-      const int piece[2] = {((2 * q) ^ g) * 16, ((2 * q + 1) ^ g) * 16};
-      const int scale_off = kWTile + q * 512 + (8 * rg + g) * 16;
-      for (int i = wk; i < n_st; i += kKWarps) {
-        const uint32_t it = it0 + i, s = it % STAGES;
-        const bool mine = mbar_wait_bounded(smem_u32(&bar_full[s]), (it / STAGES) & 1u, &abort_flag);
-        if (!__all_sync(0xffffffffu, mine)) break;
-        const uint8_t* st = smem + s * C::STAGE;
-        const uint8_t* xb[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-          xb[n] = (n * 8 + g >= ntok ? zeros
-                   : XIN ? smem + C::X_AT + ((n * 8 + g) * n_st + i) * kXRow
-                         : st + kWTile + kSTile + (n * 8 + g) * kXRow) +
-                  q * 16;
-        // One step: 8 words of 8 codes per row.  The sums of a step start from zero and are added
-        // to the running sums in plain float32 (the MMA truncates as it accumulates, and over a
-        // long K that would drift).
-        uint32_t sc[4][2];
-        {
-          uint4 sv = lds16(st + scale_off);
-          // past K the codes are zeros, but the scale bytes are whatever was there
-          if ((st0 + i) * kStepK + q * 64 >= A.K) sv = make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t sw[4] = {sv.x, sv.y, sv.z, sv.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            sc[j][0] = decode_scales(sw[j] & 0xFFFFu);
-            sc[j][1] = decode_scales(sw[j] >> 16);
-          }
-        }
-        float tmp[CH][2][NT][4];
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t w[4][4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint4 v = lds16(st + row_off + j * (32 * 128) + piece[half]);
-            w[j][0] = v.x;
-            w[j][1] = v.y;
-            w[j][2] = v.z;
-            w[j][3] = v.w;
-          }
-#pragma unroll
-          for (int wd = 0; wd < 4; ++wd) {
-            uint4 b[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) b[n] = lds16(xb[n] + half * 256 + wd * 64);
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              uint32_t a[2][4];
-#pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                decode8(w[2 * p + r][wd], a[r]);
-                // the scale of 16-element group 2 * half + wd / 2, in both halves
-                const uint32_t sv =
-                    __byte_perm(sc[2 * p + r][half], 0u, (wd & 2) ? 0x3232u : 0x1010u);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) a[r][j] = mul_f16x2(a[r][j], sv);
-              }
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                auto& t0 = tmp[0][p][n];
-                auto& t1 = tmp[CH - 1][p][n];
-                if (half == 0 && wd == 0) {
-                  mma_f16_first(t0, a[0][0], a[1][0], a[0][1], a[1][1], b[n].x, b[n].y);
-                  if constexpr (CH == 2)
-                    mma_f16_first(t1, a[0][2], a[1][2], a[0][3], a[1][3], b[n].z, b[n].w);
-                  else
-                    mma_f16(t1, a[0][2], a[1][2], a[0][3], a[1][3], b[n].z, b[n].w);
-                } else {
-                  mma_f16(t0, a[0][0], a[1][0], a[0][1], a[1][1], b[n].x, b[n].y);
-                  mma_f16(t1, a[0][2], a[1][2], a[0][3], a[1][3], b[n].z, b[n].w);
-                }
-              }
-            }
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bar_empty[s]));
+      for (int c = 0; c < 2; ++c) {
+        const int t = n * 8 + 2 * q + c;
+        if (t >= ntok) continue;
+        float f0, f1;
+        gs.factors(s_exp[t], f0, f1);
 #pragma unroll
         for (int p = 0; p < 2; ++p)
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              acc[p][n][j] += tmp[0][p][n][j];
-              if (CH == 2) acc[p][n][j] += tmp[CH - 1][p][n][j];
-            }
+          for (int r = 0; r < 2; ++r)
+            red[(wk * TOK + t) * kRedStride + 8 * rg + g + 64 * p + 32 * r] =
+                acc[p][n][2 * r + c] * f0 * f1;
       }
-    }
-
-    // partial sums of the K warps (and of the cluster's CTAs) -> shared memory, added in order
-    __syncthreads();
-    float* red = reinterpret_cast<float*>(smem);  // [kKWarps][TOK][kRedStride]
-    if (warp < kConsumers) {
-      const int rg = warp % kRowWarps, wk = warp / kRowWarps;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int t = n * 8 + 2 * q + c;
-          if (t >= ntok) continue;
-          // undo the row's power of two and the one in the global scale, in two exact steps (the
-          // rest of the global scale, in [1, 2), divides the total)
-          const int up = -s_exp[t] - gs_exp;  // within [-253, 240]
-          const float f0 = pow2f(up / 2), f1 = pow2f(up - up / 2);
-#pragma unroll
-          for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              red[(wk * TOK + t) * kRedStride + 8 * rg + g + 64 * p + 32 * r] =
-                  acc[p][n][2 * r + c] * f0 * f1;
-            }
-        }
-    }
-    if (A.splits > 1) cluster_sync();
-    else __syncthreads();
-    auto total = [&](int row, int t) {
+  }
+  if (A.splits > 1) cluster_sync();
+  else __syncthreads();
+  const int share = 128 / A.splits, r0 = share * split;
+  if (!abort_flag) {
+    for (int idx = tid; idx < share * ntok; idx += kThreads) {
+      const int row = r0 + idx % share, t = idx / share, n = rowblk * 128 + row;
       const float* at = red + t * kRedStride + row;
       float v = 0.0f;
       if (A.splits > 1) {
@@ -653,89 +699,352 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT, XIN>::CTAS)
 #pragma unroll
         for (int w = 0; w < kKWarps; ++w) v += at[w * TOK * kRedStride];
       }
-      return v / gs_frac;
-    };
-    const int share = 128 / A.splits, r0 = share * split;
-    if (!abort_flag) {
-      if constexpr (MODE == FFN_L1) {
-        // gate rows 32j + i, up rows 32j + 16 + i -> feature 16j + i
-        const int feats = share / 2, I = A.N / 2;
-        for (int idx = tid; idx < feats * ntok; idx += kThreads) {
-          const int f = idx % feats, t = idx / feats;
-          const int row = r0 + (f / 16) * 32 + f % 16;
-          const float gate = total(row, t), up = total(row + 16, t);
-          static_cast<float*>(A.out)[(int64_t)s_row[t] * I + (rowblk * 128 + r0) / 2 + f] =
-              gate * up / (1.0f + expf(-gate));
-        }
-      } else {
-        for (int idx = tid; idx < share * ntok; idx += kThreads) {
-          const int row = r0 + idx % share, t = idx / share;
-          const int n = rowblk * 128 + row;
-          const float v = total(row, t);
-          if (n < A.N) {
-            const int64_t at = (int64_t)s_row[t] * A.N + n;
-            if (MODE == FFN_L2 || A.out_f32) static_cast<float*>(A.out)[at] = v;
-            else static_cast<__nv_bfloat16*>(A.out)[at] = __float2bfloat16_rn(v);
-          }
-        }
+      v /= gs.frac;
+      if (n < W.N) {
+        const int64_t o = (int64_t)(m0 + t) * W.N + n;
+        if (A.out_f32) static_cast<float*>(A.out)[o] = v;
+        else static_cast<__nv_bfloat16*>(A.out)[o] = __float2bfloat16_rn(v);
       }
     }
-    // the peers have read this CTA's sums before it leaves, and its threads before the next
-    // token block's copies overwrite them
-    if (tb + 1 < tb_last) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    if (A.splits > 1) cluster_sync();
-    else __syncthreads();
   }
+  if (A.splits > 1) cluster_sync();  // the peers have read this CTA's sums
   if (tid == 0 && abort_flag) report(A.status, NVFP4_DEVERR_TIMEOUT);
 }
 
-// out[t] = sum over the token's live slots of w * ys[slot], in slot order, FP32 -> bf16.  Lane j of
-// a warp holds slot j's id and weight (k <= 32).
-__global__ void __launch_bounds__(256) combine_slots_kernel(const float* ys, const int32_t* ids,
-                                                            const float* w, int H, int E, int k,
-                                                            __nv_bfloat16* out) {
-  pdl_wait();
-  const int t = blockIdx.x, lane = threadIdx.x & 31;
-  int live = 0;
-  float wl = 0.0f;
-  if (lane < k) {
-    const int id = ld_after(ids + t * k + lane);
-    live = id >= 0 && id < E;
-    if (live) wl = __int_as_float(ld_after(reinterpret_cast<const int32_t*>(w) + t * k + lane));
+// ------------------------------------------------------------------------ streamed, in even shares
+
+// For many output blocks: the blocks (a unit of up to 8 * NT tokens against 128 weight rows) follow
+// one another, each ceil(K / 256) steps long, and every CTA takes the same number of consecutive
+// steps, wherever its share starts and ends.  A CTA's copies run on across blocks.  What a K warp
+// sums of a block goes to a plane of its own: `part` holds [row][planes][blocks * 128], plane
+// 2 * piece + K warp, a block's pieces counted from the CTA that starts it.  The kernel behind
+// adds a block's planes in order.
+enum Mode { DENSE = 0, FFN_L1 = 1, FFN_L2 = 2 };
+constexpr int kStreamCtas = 2 * 148;  // two per SM, all resident at once
+
+struct Split {
+  int blocks;   // of 128 weight rows
+  int steps;    // of a block
+  int planes;   // of a row, at most
+  int least;    // steps of a CTA
+  int units;    // DENSE; the FFN's are counted on the device
+  // (the host sees to it that the steps of all blocks fit 31 bits)
+  __host__ __device__ int per_cta(int n_units) const {
+    const int total = n_units * blocks * steps;
+    const int per = static_cast<int>((static_cast<unsigned>(total) + kStreamCtas - 1) / kStreamCtas);
+    return per > least ? per : least;
   }
-  const uint32_t mask = __ballot_sync(0xffffffffu, live);
-  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * 4;
-  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  constexpr int kAhead = 8;  // slots whose loads are in flight together
-  for (int j0 = 0; j0 < k; j0 += kAhead) {
-    uint4 y[kAhead];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-      if (j0 + j < k && c < H && ((mask >> (j0 + j)) & 1u))
-        y[j] = ld_after16(ys + ((int64_t)t * k + j0 + j) * H + c);
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const float wj = __shfl_sync(0xffffffffu, wl, (j0 + j) & 31);
-      if (j0 + j < k && c < H && ((mask >> (j0 + j)) & 1u)) {
-        v[0] += wj * __uint_as_float(y[j].x);
-        v[1] += wj * __uint_as_float(y[j].y);
-        v[2] += wj * __uint_as_float(y[j].z);
-        v[3] += wj * __uint_as_float(y[j].w);
+};
+// planes that hold something of block b
+__device__ __forceinline__ int block_planes(const Split& S, int per, int b) {
+  return kKWarps * (((b + 1) * S.steps - 1) / per - b * S.steps / per + 1);
+}
+
+struct StreamArgs {
+  Split split;
+  int M;                  // DENSE: rows of x
+  int k;                  // FFN: slots per token
+  const int4* plan;       // FFN: {expert, first, count, 0} per unit
+  const int32_t* n_plan;  // and how many there are
+  const int32_t* order;   // slots sorted by expert
+  float* part;
+  int32_t* status;
+};
+
+template <int NT, Mode MODE>
+__global__ void __launch_bounds__(kThreads, 2)
+    stream_kernel(const __grid_constant__ CUtensorMap tm, const Operands W, const StreamArgs A) {
+  using C = Cfg<NT, false>;
+  constexpr int TOK = C::TOK, STAGES = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  __shared__ __align__(8) uint64_t bar_full[STAGES], bar_empty[STAGES];
+  __shared__ volatile int abort_flag;
+  __shared__ __align__(16) uint8_t zeros[kStepX];  // what columns without a token read
+  const Ring<STAGES> ring{bar_full, bar_empty, &abort_flag};
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, q = lane & 3;
+  if (tid == 0) ring.init();
+  if (tid < kStepX / 16) reinterpret_cast<uint4*>(zeros)[tid] = make_uint4(0u, 0u, 0u, 0u);
+  __syncthreads();
+  // The L2 form's plan is older than the kernel it waits for (the one that makes the
+  // intermediate, behind the L1, which started after the plan was complete), so it is read before
+  // that wait and the first weights are on their way during it.
+  if constexpr (MODE == FFN_L1) pdl_wait();
+  const Split& S = A.split;
+  const int units = MODE == DENSE ? S.units : ld_after(A.n_plan);
+  pdl_trigger();
+  const int total = units * S.blocks * S.steps, per = S.per_cta(units);
+  const int lo = static_cast<int>(min((int64_t)total, (int64_t)per * blockIdx.x));
+  const int hi = static_cast<int>(min((int64_t)total, (int64_t)lo + per)), n = hi - lo;
+  if (n == 0) {
+    pdl_wait();  // no kernel of the chain ends before the ones in front of it
+    return;
+  }
+  const int atoms_k = W.K / 64;
+
+  // a block's unit and weight rows: the dense form goes through the units of one weight block, the
+  // FFN through the weight blocks of one unit
+  struct Block {
+    int rowblk, e, first, count;
+  };
+  auto block = [&](int b) {
+    Block k;
+    if constexpr (MODE == DENSE) {
+      k.rowblk = b / units;
+      k.e = 0;
+      k.first = b % units * TOK;
+      k.count = min(TOK, A.M - k.first);
+    } else {
+      k.rowblk = b % S.blocks;
+      const uint4 p = ld_after16(A.plan + b / S.blocks);
+      k.e = static_cast<int>(p.x);
+      k.first = static_cast<int>(p.y);
+      k.count = static_cast<int>(p.z);
+    }
+    return k;
+  };
+  auto out_row = [&](const Block& k, int t) {  // DENSE: the row of x; FFN: the slot
+    return MODE == DENSE ? k.first + t : ld_after(A.order + k.first + t);
+  };
+  auto x_row = [&](int r) { return MODE == FFN_L1 ? r / A.k : r; };
+
+  if (warp == kConsumers) {
+    // =========================== copies ===========================
+    auto stage = [&](int i) { return smem + (i % STAGES) * C::STAGE; };
+    struct Cursor {
+      int b, st;
+      Block k;
+      const uint8_t *sf, *x;
+    };
+    auto enter = [&](Cursor& c, bool with_x) {
+      c.k = block(c.b);
+      c.sf = W.sf + ((int64_t)c.k.e * S.blocks + c.k.rowblk) * atoms_k * 512;
+      if (with_x && lane < c.k.count)
+        c.x = W.xf + (int64_t)x_row(out_row(c.k, lane)) * S.steps * kStepX;
+    };
+    auto advance = [&](Cursor& c, bool with_x) {
+      if (++c.st == S.steps) {
+        c.st = 0;
+        if (++c.b * S.steps < hi) enter(c, with_x);
       }
+    };
+    auto copy_w = [&](int i, const Cursor& c) {
+      ring.copy_w(i, stage(i), &tm, c.k.e * W.N + c.k.rowblk * 128, c.sf, c.st, atoms_k,
+                  c.k.count * kStepX);
+    };
+    auto copy_x = [&](int i, const Cursor& c) {
+      if (lane < c.k.count) ring.copy_x(i, stage(i), c.x + (int64_t)c.st * kStepX);
+    };
+    Cursor c{lo / S.steps, lo % S.steps, {}, nullptr, nullptr};
+    Cursor early = c;
+    enter(early, false);
+    const int head = min(n, STAGES);
+    for (int i = 0; i < head; ++i) {  // while the activations are being made
+      copy_w(i, early);
+      advance(early, false);
+    }
+    pdl_wait();
+    enter(c, true);
+    bool ok = true;
+    int i = 0;
+    for (; i < n; ++i) {
+      if (i >= head) {
+        ok = ring.wait_empty(i);
+        if (!ok) break;
+        copy_w(i, c);
+      }
+      copy_x(i, c);
+      advance(c, true);
+    }
+    if (!ok) ring.drain(i);
+  } else {
+    // =========================== products ===========================
+    const int rg = warp % kRowWarps, wk = warp / kRowWarps;
+    const Lane<NT> me(rg, lane);
+    const int64_t n_pad = (int64_t)S.blocks * 128;
+    pdl_wait();
+    bool ok = true;
+    for (int it = 0; it < n && ok;) {
+      const int b = (lo + it) / S.steps, s0 = (lo + it) % S.steps, len = min(S.steps - s0, n - it);
+      const Block k = block(b);
+      const float gs_value = __ldg(W.gs + k.e);
+      // this lane's two columns of every token tile
+      int row[NT][2], row_exp[NT][2];
+#pragma unroll
+      for (int t8 = 0; t8 < NT; ++t8)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int t = t8 * 8 + 2 * q + c;
+          row[t8][c] = t < k.count ? out_row(k, t) : -1;
+          row_exp[t8][c] = row[t8][c] >= 0 ? ld_after(W.exps + x_row(row[t8][c])) : 0;
+        }
+      float acc[2][NT][4];
+      clear<NT>(acc);
+      for (int i = (it + wk) & 1; i < len; i += kKWarps) {  // the stages it + i with (it + i) % 2 == wk
+        if (!ring.wait_full(it + i)) {
+          ok = false;
+          break;
+        }
+        const uint8_t* st = smem + ((it + i) % STAGES) * C::STAGE;
+        const uint8_t* xb[NT];
+#pragma unroll
+        for (int t8 = 0; t8 < NT; ++t8)
+          xb[t8] = (t8 * 8 + g < k.count ? st + kWTile + kSTile + (t8 * 8 + g) * kXRow : zeros) + q * 16;
+        me.step(st, xb, W.K - (s0 + i) * kStepK, acc);
+        ring.release(it + i);
+      }
+      it += len;
+      const GlobalScale gs(gs_value);
+      const int plane = (static_cast<int>(blockIdx.x) - b * S.steps / per) * kKWarps + wk;
+#pragma unroll
+      for (int t8 = 0; t8 < NT; ++t8)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (row[t8][c] < 0) continue;
+          float f0, f1;
+          gs.factors(row_exp[t8][c], f0, f1);
+          float* d = A.part + ((int64_t)row[t8][c] * S.planes + plane) * n_pad + k.rowblk * 128 +
+                     8 * rg + g;
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              d[64 * p + 32 * r] = acc[p][t8][2 * r + c] * f0 * f1 / gs.frac;
+        }
     }
   }
-  if (c >= H) return;
-  __nv_bfloat162 o[2] = {__floats2bfloat162_rn(v[0], v[1]), __floats2bfloat162_rn(v[2], v[3])};
-  *reinterpret_cast<uint2*>(out + (int64_t)t * H + c) = *reinterpret_cast<const uint2*>(o);
+  __syncthreads();
+  if (tid == 0 && abort_flag) report(A.status, NVFP4_DEVERR_TIMEOUT);
+}
+
+// Sums over a block's planes, in order, of V groups of 4 consecutive columns; the loads of 16 / V
+// planes are in flight together.
+template <int V>
+__device__ __forceinline__ void sum_planes(const float* base, const int (&at)[V], int64_t n_pad,
+                                           int planes, float (&v)[V][4]) {
+  constexpr int kAhead = 16 / V;
+#pragma unroll
+  for (int g = 0; g < V; ++g)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[g][i] = 0.0f;
+  for (int a = 0; a < planes; a += kAhead) {
+    uint4 q[kAhead][V];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+      for (int g = 0; g < V; ++g)
+        if (a + j < planes) q[j][g] = ld_after16(base + (a + j) * n_pad + at[g]);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+      for (int g = 0; g < V; ++g)
+        if (a + j < planes) {
+          v[g][0] += __uint_as_float(q[j][g].x);
+          v[g][1] += __uint_as_float(q[j][g].y);
+          v[g][2] += __uint_as_float(q[j][g].z);
+          v[g][3] += __uint_as_float(q[j][g].w);
+        }
+  }
+}
+
+// The dense form's output from its planes: 4 columns of a row of x per thread.
+__global__ void __launch_bounds__(128) dense_sum_kernel(const float* part, const Split S, int tok,
+                                                        int N, void* out, int out_f32) {
+  pdl_wait();
+  const int m = blockIdx.y, c = (blockIdx.x * blockDim.x + threadIdx.x) * 4;
+  if (c >= N) return;
+  const int64_t n_pad = (int64_t)S.blocks * 128;
+  const int per = S.per_cta(S.units);
+  float v[1][4];
+  sum_planes<1>(part + (int64_t)m * S.planes * n_pad, {c}, n_pad,
+                block_planes(S, per, c / 128 * S.units + m / tok), v);
+  const int64_t o = (int64_t)m * N + c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (c + i >= N) break;
+    if (out_f32) static_cast<float*>(out)[o + i] = v[0][i];
+    else static_cast<__nv_bfloat16*>(out)[o + i] = __float2bfloat16_rn(v[0][i]);
+  }
+}
+
+// The FFN's intermediate of one slot per CTA: the L1's planes added, h = silu(gate) * up, and its
+// conversion for the L2.  Gate rows 32j + i and up rows 32j + 16 + i make feature 16j + i.
+__global__ void __launch_bounds__(512) swiglu_kernel(const float* part, const Split S,
+                                                     const int32_t* n_plan,
+                                                     const int32_t* slot_unit, int I, uint8_t* hf,
+                                                     int32_t* exps) {
+  __shared__ uint32_t red[32];
+  pdl_trigger();
+  pdl_wait();
+  const int64_t s = blockIdx.x;
+  const int unit = ld_after(slot_unit + s);
+  if (unit < 0) return;  // dropped
+  const int64_t n_pad = (int64_t)S.blocks * 128;
+  const int per = S.per_cta(ld_after(n_plan));
+  const int64_t steps = (I + kStepK - 1) / kStepK;
+  const float* base = part + s * S.planes * n_pad;
+  convert_row<4, 1>(
+      [&](int p, float (&h)[4]) {
+        const int f = p * 4, row = 32 * (f / 16) + f % 16;
+        float v[2][4];  // gate, up
+        sum_planes<2>(base, {row, row + 16}, n_pad,
+                      block_planes(S, per, unit * S.blocks + row / 128), v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = v[0][i] * v[1][i] / (1.0f + expf(-v[0][i]));
+      },
+      I, hf + s * steps * kStepX, exps + s, red);
+}
+
+// out[t] = sum over the token's live slots, in order, of w * (the L2's planes added).  128 columns of a
+// token per CTA: a warp takes every 8th slot, 4 columns a lane.
+constexpr int kCombineWarps = 8;
+__global__ void __launch_bounds__(32 * kCombineWarps) combine_slots_kernel(
+    const float* part, const Split S, const int32_t* n_plan, const int32_t* slot_unit,
+    const float* w, int H, int k, __nv_bfloat16* out) {
+  __shared__ float4 s_y[kCombineWarps][32];
+  pdl_wait();
+  const int64_t t = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.y * 128 + lane * 4;
+  const int64_t n_pad = (int64_t)S.blocks * 128;
+  const int per = S.per_cta(ld_after(n_plan));
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int j0 = 0; j0 < k; j0 += kCombineWarps) {
+    const int j = j0 + warp;
+    float4 wy = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const int unit = j < k ? ld_after(slot_unit + t * k + j) : -1;
+    if (unit >= 0) {
+      const float wj = __int_as_float(ld_after(reinterpret_cast<const int32_t*>(w) + t * k + j));
+      float y[1][4];
+      sum_planes<1>(part + (t * k + j) * S.planes * n_pad, {c}, n_pad,
+                    block_planes(S, per, unit * S.blocks + blockIdx.y), y);
+      wy = make_float4(wj * y[0][0], wj * y[0][1], wj * y[0][2], wj * y[0][3]);
+    }
+    s_y[warp][lane] = wy;
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int i = 0; i < kCombineWarps; ++i) {
+        const float4 y = s_y[i][lane];
+        v[0] += y.x;
+        v[1] += y.y;
+        v[2] += y.z;
+        v[3] += y.w;
+      }
+    }
+    __syncthreads();
+  }
+  if (warp != 0) return;
+  const __nv_bfloat162 o[2] = {__floats2bfloat162_rn(v[0], v[1]), __floats2bfloat162_rn(v[2], v[3])};
+  *reinterpret_cast<uint2*>(out + t * H + c) = *reinterpret_cast<const uint2*>(o);
 }
 
 // ------------------------------------------------------------------------------ host side
 
-// The SM count the K splits are sized for (on another device they are only less well chosen).
-constexpr int kSizingSms = 148;
+constexpr int kSizingSms = 148;  // the SM count the K splits are sized for
 
-// CTAs along K for one output block: enough CTAs for every SM, while each K warp keeps
-// at least one step.
+// CTAs along K for one output block: enough CTAs for every SM, while each K warp keeps at least one
+// step.
 int pick_splits(int64_t blocks, int K, int most) {
   const int steps = (K + kStepK - 1) / kStepK;
   int s = 1;
@@ -744,8 +1053,8 @@ int pick_splits(int64_t blocks, int K, int most) {
 }
 
 template <typename... P, typename... V>
-nvfp4_status_t launch_after(void (*fn)(P...), dim3 grid, int threads, size_t smem, int cluster,
-                            bool early, cudaStream_t s, const char* what, const V&... args) {
+nvfp4_status_t launch(void (*fn)(P...), dim3 grid, int threads, size_t smem, int cluster, bool early,
+                      cudaStream_t s, const char* what, const V&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
@@ -769,22 +1078,17 @@ nvfp4_status_t launch_after(void (*fn)(P...), dim3 grid, int threads, size_t sme
   return check_launch(what);
 }
 
-template <int NT, Mode MODE, bool XIN>
-nvfp4_status_t launch(const CUtensorMap& tm, const Args& a, dim3 grid, bool early,
-                      cudaStream_t s) {
-  auto* fn = w4a16_kernel<NT, MODE, XIN>;
-  constexpr int smem = Cfg<NT, XIN>::SMEM;
-  // the attribute is set once per device (a call costs about as much as a launch)
-  static std::atomic<uint64_t> devices_set{0};
+// Lets fn use `smem` bytes, once per device (a call costs about as much as a launch).
+template <typename Fn>
+bool allow_smem(Fn fn, int smem, std::atomic<uint64_t>& devices_set) {
   int dev = 0;
   cudaGetDevice(&dev);
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (!(devices_set.load(std::memory_order_acquire) & bit)) {
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-      return check_launch("w4a16_kernel attributes");
-    devices_set.fetch_or(bit, std::memory_order_release);
-  }
-  return launch_after(fn, grid, kThreads, smem, a.splits, early, s, "w4a16_kernel", tm, a);
+  if (devices_set.load(std::memory_order_acquire) & bit) return true;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return false;
+  devices_set.fetch_or(bit, std::memory_order_release);
+  return true;
 }
 
 bool weight_map(CUtensorMap* tm, const uint8_t* codes, int64_t rows, int K) {
@@ -794,22 +1098,50 @@ bool weight_map(CUtensorMap* tm, const uint8_t* codes, int64_t rows, int K) {
   return false;
 }
 
-// The product kernel over weights `codes` of `rows` rows, behind the kernel of this call that
-// converts its activations.
-template <Mode MODE>
-nvfp4_status_t launch_nt(int nt, const uint8_t* codes, int64_t rows, const Args& a, dim3 grid,
-                         cudaStream_t s) {
+template <int NT, bool XIN>
+nvfp4_status_t launch_dense(const uint8_t* codes, const Operands& w, const DenseArgs& a, dim3 grid,
+                            cudaStream_t s) {
+  constexpr int smem = Cfg<NT, XIN>::SMEM;
+  static std::atomic<uint64_t> devices_set{0};
+  if (!allow_smem(dense_kernel<NT, XIN>, smem, devices_set)) return check_launch("dense_kernel");
   CUtensorMap tm;
-  if (!weight_map(&tm, codes, rows, a.K)) return NVFP4_ERR_CUDA;
-  switch (nt) {
-    case 1: return launch<1, MODE, false>(tm, a, grid, true, s);
-    case 2: return launch<2, MODE, false>(tm, a, grid, true, s);
-    default: return launch<4, MODE, false>(tm, a, grid, true, s);
-  }
+  if (!weight_map(&tm, codes, w.N, w.K)) return NVFP4_ERR_CUDA;
+  return launch(dense_kernel<NT, XIN>, grid, kThreads, smem, a.splits, !XIN, s, "dense_kernel", tm, w,
+                a);
+}
+
+template <int NT, Mode MODE>
+nvfp4_status_t launch_stream(const uint8_t* codes, int64_t rows, const Operands& w,
+                             const StreamArgs& a, cudaStream_t s) {
+  constexpr int smem = Cfg<NT, false>::SMEM;
+  static std::atomic<uint64_t> devices_set{0};
+  if (!allow_smem(stream_kernel<NT, MODE>, smem, devices_set)) return check_launch("stream_kernel");
+  CUtensorMap tm;
+  if (!weight_map(&tm, codes, rows, w.K)) return NVFP4_ERR_CUDA;
+  return launch(stream_kernel<NT, MODE>, dim3(kStreamCtas), kThreads, smem, 1, true, s,
+                "stream_kernel", tm, w, a);
+}
+template <Mode MODE>
+nvfp4_status_t launch_stream(int nt, const uint8_t* codes, int64_t rows, const Operands& w,
+                             const StreamArgs& a, cudaStream_t s) {
+  return nt == 1 ? launch_stream<1, MODE>(codes, rows, w, a, s)
+                 : launch_stream<2, MODE>(codes, rows, w, a, s);
 }
 
 int64_t converted_bytes(int64_t rows, int K) {
   return rows * ((K + kStepK - 1) / kStepK) * kStepX;
+}
+
+// Shares of at least `least` steps.
+Split make_split(int N, int K, int64_t least, int units) {
+  Split S{};
+  S.blocks = static_cast<int>(((int64_t)N + 127) / 128);
+  S.steps = (K + kStepK - 1) / kStepK;
+  S.least = static_cast<int>(least);
+  S.units = units;
+  // shares of at least `least` steps that a block of S.steps can lie in
+  S.planes = kKWarps * (S.steps == 1 ? 1 : (S.steps - 2) / S.least + 2);
+  return S;
 }
 
 // How nvfp4_linear_w4a16 runs a shape, and the byte offsets of its workspace regions (256-byte
@@ -817,52 +1149,81 @@ int64_t converted_bytes(int64_t rows, int K) {
 struct LinearW4Plan {
   int nt, splits;
   int64_t rowblks, tblks;
-  bool xin;
-  int64_t exps, total;
+  bool xin, stream;
+  Split split;
+  int64_t exps, part, total;
 };
+
+// The streamed form takes products of at least this many steps per CTA and at most this many rows
+// (its planes are float32 [rows][planes][N]).  TBD
+constexpr int kStreamMinSteps = 8;
+constexpr int kStreamMaxRows = 64;
 
 LinearW4Plan linear_w4_plan(int64_t M, int N, int K) {
   LinearW4Plan P{};
-  P.nt = M <= 8 ? 1 : M <= 16 ? 2 : 4;
+  P.nt = M <= 8 ? 1 : 2;
   P.rowblks = ((int64_t)N + 127) / 128;
   P.tblks = (M + 8 * P.nt - 1) / (8 * P.nt);
-  P.splits = pick_splits(P.rowblks * P.tblks, K, kMaxSplits);
-  const int steps = (K + kStepK - 1) / kStepK;
-  P.xin = P.nt == 1 && M * ((steps + P.splits - 1) / P.splits) <= kMaxPieces;
+  const int64_t steps = (K + kStepK - 1) / kStepK, total = P.rowblks * P.tblks * steps;
+  P.stream = M <= kStreamMaxRows && total >= (int64_t)kStreamMinSteps * kStreamCtas &&
+             total <= INT32_MAX;
+  if (P.stream) {
+    // every CTA's share is known here, so `least` is the share itself
+    P.split = make_split(N, K, (total + kStreamCtas - 1) / kStreamCtas, static_cast<int>(P.tblks));
+  } else {
+    P.splits = pick_splits(P.rowblks * P.tblks, K, kMaxSplits);
+    P.xin = P.nt == 1 && M * ((steps + P.splits - 1) / P.splits) <= kMaxPieces;
+  }
   if (!P.xin) {
     P.exps = round_up(converted_bytes(M, K), 256);
-    P.total = P.exps + round_up(M * 4, 256);
+    P.part = P.exps + round_up(M * 4, 256);
+    P.total = P.part;
+    if (P.stream) P.total += round_up(M * P.split.planes * P.rowblks * 128 * 4, 256);
   }
   return P;
 }
 
-// Byte offsets of the moe_ffn_w4a16 workspace regions (each 256-byte aligned).
-struct FfnW4Layout {
-  int64_t ids, w, plan, n_plan, order, xf, xexp, h, hf, hexp, ys, total;
+// How moe_ffn_w4a16 runs a shape, and the byte offsets of its workspace regions (256-byte aligned).
+struct FfnW4Plan {
+  int nt;
+  Split l1, l2;
+  int64_t ids, w, plan, n_plan, order, slot_unit, xf, xexp, hf, hexp, part, total;
 };
 
-FfnW4Layout ffn_w4_layout(int T, int H, int I, int E, int k) {
-  FfnW4Layout L{};
+FfnW4Plan ffn_w4_plan(int T, int H, int I, int E, int k) {
+  FfnW4Plan P{};
   const int64_t S = (int64_t)T * k;
+  // token tiles: twice what an expert gets on average
+  P.nt = 2 * S / E <= 8 ? 1 : 2;
+  // With few slots a share may be as short as 4 steps, so that a handful of experts still occupies
+  // every CTA; with more, whole blocks (2 pieces at most), which keeps the planes small.
+  auto split = [&](int N, int K) {
+    const int steps = (K + kStepK - 1) / kStepK;
+    return make_split(N, K, S <= 64 && steps > 4 ? 4 : steps, 0);
+  };
+  P.l1 = split(2 * I, H);
+  P.l2 = split(H, I);
   int64_t o = 0;
   auto take = [&](int64_t bytes) {
     const int64_t at = o;
     o = round_up(o + bytes, 256);
     return at;
   };
-  L.ids = take(S * 4);
-  L.w = take(S * 4);
-  L.plan = take((int64_t)E * 16);
-  L.n_plan = take(4);
-  L.order = take(S * 4);
-  L.xf = take(converted_bytes(T, H));
-  L.xexp = take((int64_t)T * 4);
-  L.h = take(S * I * 4);
-  L.hf = take(converted_bytes(S, I));
-  L.hexp = take(S * 4);
-  L.ys = take(S * H * 4);
-  L.total = o;
-  return L;
+  P.ids = take(S * 4);
+  P.w = take(S * 4);
+  P.plan = take(S * 16);
+  P.n_plan = take(4);
+  P.order = take(S * 4);
+  P.slot_unit = take(S * 4);
+  P.xf = take(converted_bytes(T, H));
+  P.xexp = take((int64_t)T * 4);
+  P.hf = take(converted_bytes(S, I));
+  P.hexp = take(S * 4);
+  // the L1's planes, then the L2's (which writes after the intermediate has been made)
+  const int64_t p1 = S * P.l1.planes * P.l1.blocks, p2 = S * P.l2.planes * P.l2.blocks;
+  P.part = take((p1 > p2 ? p1 : p2) * 128 * 4);
+  P.total = o;
+  return P;
 }
 
 }  // namespace
@@ -882,7 +1243,7 @@ extern "C" nvfp4_status_t nvfp4_linear_w4a16(const void* x, int64_t M, int K, in
                                              nvfp4_stream_t stream) {
   if (M < 0 || N <= 0 || K <= 0 || ld < K || (out_dtype != 0 && out_dtype != 1))
     return NVFP4_ERR_INVALID_ARG;
-  if (K % 64 || ld % 8 || M > (int64_t)65535 * 32 || N > INT32_MAX - 127)
+  if (K % 64 || ld % 8 || M > (int64_t)65535 * 16 || N > INT32_MAX - 127)
     return NVFP4_ERR_UNSUPPORTED_SHAPE;
   if (!w || !sfw || !gs_w) return NVFP4_ERR_INVALID_ARG;
   if (M > 0 && (!x || !out)) return NVFP4_ERR_INVALID_ARG;
@@ -895,36 +1256,36 @@ extern "C" nvfp4_status_t nvfp4_linear_w4a16(const void* x, int64_t M, int K, in
   if (M == 0) return NVFP4_OK;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(ws);
-  Args a{};
-  a.sf = sfw;
-  a.gs = gs_w;
-  a.N = N;
-  a.K = K;
-  a.x = x;
-  a.ld_bytes = ld * 2;
-  a.M = static_cast<int>(M);
-  a.out = out;
-  a.out_f32 = out_dtype == 0;
-  a.splits = P.splits;
-  a.status = dev_status;
-  const dim3 grid(static_cast<unsigned>(P.rowblks * P.splits), static_cast<unsigned>(P.tblks));
-  if (P.xin) {
-    CUtensorMap tm;
-    if (!weight_map(&tm, w, N, K)) return NVFP4_ERR_CUDA;
-    return launch<1, DENSE, true>(tm, a, grid, false, s);
+  int32_t* exps = reinterpret_cast<int32_t*>(base + P.exps);
+  if (!P.xin) {
+    const nvfp4_status_t st =
+        launch(convert_kernel, dim3(static_cast<unsigned>(M)), 256, 0, 1, false, s, "convert_kernel",
+               static_cast<const uint8_t*>(x), ld * 2, K, base, exps);
+    if (st != NVFP4_OK) return st;
   }
-  a.xf = base;
-  a.exps = reinterpret_cast<const int32_t*>(base + P.exps);
-  convert_kernel<false><<<static_cast<unsigned>(M), 256, 0, s>>>(
-      x, ld * 2, K, base, reinterpret_cast<int32_t*>(base + P.exps));
-  const nvfp4_status_t st = check_launch("convert_kernel");
-  if (st != NVFP4_OK) return st;
-  return launch_nt<DENSE>(P.nt, w, N, a, grid, s);
+  const Operands op{sfw, gs_w, N, K, base, exps};
+  if (P.stream) {
+    StreamArgs a{};
+    a.split = P.split;
+    a.M = static_cast<int>(M);
+    a.part = reinterpret_cast<float*>(base + P.part);
+    a.status = dev_status;
+    const nvfp4_status_t st = launch_stream<DENSE>(P.nt, w, N, op, a, s);
+    if (st != NVFP4_OK) return st;
+    return launch(dense_sum_kernel, dim3((N / 4 + 128) / 128, static_cast<unsigned>(M)), 128, 0, 1,
+                  true, s, "dense_sum_kernel", a.part, P.split, 8 * P.nt, N, out,
+                  static_cast<int>(out_dtype == 0));
+  }
+  const DenseArgs a{x, ld * 2, static_cast<int>(M), out, out_dtype == 0, P.splits, dev_status};
+  const dim3 grid(static_cast<unsigned>(P.rowblks * P.splits), static_cast<unsigned>(P.tblks));
+  if (P.xin) return launch_dense<1, true>(w, op, a, grid, s);
+  return P.nt == 1 ? launch_dense<1, false>(w, op, a, grid, s)
+                   : launch_dense<2, false>(w, op, a, grid, s);
 }
 
 extern "C" size_t moe_ffn_w4a16_workspace_size(int T, int H, int I, int E, int k) {
   if (T < 0 || H <= 0 || I <= 0 || E <= 0 || k <= 0) return 0;
-  return static_cast<size_t>(ffn_w4_layout(T, H, I, E, k).total);
+  return static_cast<size_t>(ffn_w4_plan(T, H, I, E, k).total);
 }
 
 extern "C" nvfp4_status_t moe_ffn_w4a16(const void* x_bf16, const float* logits,
@@ -944,8 +1305,10 @@ extern "C" nvfp4_status_t moe_ffn_w4a16(const void* x_bf16, const float* logits,
     return NVFP4_ERR_INVALID_ARG;
   if (logits == nullptr ? (!topk_ids || !topk_w) : (topk_ids || topk_w))
     return NVFP4_ERR_INVALID_ARG;  // logits, or a given routing: exactly one of them
-  const FfnW4Layout L = ffn_w4_layout(T, H, I, E, k);
-  if (ws_bytes < static_cast<size_t>(L.total)) return NVFP4_ERR_WORKSPACE_TOO_SMALL;
+  const FfnW4Plan P = ffn_w4_plan(T, H, I, E, k);
+  for (const Split& l : {P.l1, P.l2})  // a unit holds a slot at least
+    if ((int64_t)T * k * l.blocks * l.steps > INT32_MAX) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (ws_bytes < static_cast<size_t>(P.total)) return NVFP4_ERR_WORKSPACE_TOO_SMALL;
   const void* ptrs16[] = {x_bf16, w1, sfw1, w2, sfw2, out_bf16};
   for (const void* p : ptrs16)
     if (!aligned16(p)) return NVFP4_ERR_MISALIGNED;
@@ -956,51 +1319,34 @@ extern "C" nvfp4_status_t moe_ffn_w4a16(const void* x_bf16, const float* logits,
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(ws);
   auto i32 = [&](int64_t off) { return reinterpret_cast<int32_t*>(base + off); };
-  auto f32 = [&](int64_t off) { return reinterpret_cast<float*>(base + off); };
-  int32_t* ids = logits != nullptr ? i32(L.ids) : const_cast<int32_t*>(topk_ids);
-  float* wts = logits != nullptr ? f32(L.w) : const_cast<float*>(topk_w);
-  int4* plan = reinterpret_cast<int4*>(base + L.plan);
-  plan_kernel<<<1 + T, 512, 0, s>>>(logits, T, E, k, ids, wts, plan, i32(L.n_plan), i32(L.order),
-                                    x_bf16, H, base + L.xf, i32(L.xexp), dev_status);
-  nvfp4_status_t st = check_launch("plan_kernel");
+  int32_t* ids = logits != nullptr ? i32(P.ids) : const_cast<int32_t*>(topk_ids);
+  float* wts = logits != nullptr ? reinterpret_cast<float*>(base + P.w) : const_cast<float*>(topk_w);
+  int4* plan = reinterpret_cast<int4*>(base + P.plan);
+  const int S = T * k;
+  nvfp4_status_t st =
+      launch(plan_kernel, dim3(1 + T), kPlanThreads, 0, 1, false, s, "plan_kernel", logits, T, E, k,
+             8 * P.nt, ids, wts, plan, i32(P.n_plan), i32(P.order), i32(P.slot_unit),
+             static_cast<const uint8_t*>(x_bf16), H, base + P.xf, i32(P.xexp), dev_status);
   if (st != NVFP4_OK) return st;
-  const int S = T * k, busy = S < E ? S : E;
-  // token tiles: twice what an expert gets on average
-  const int per = 2 * S / E;
-  const int nt = per <= 8 ? 1 : per <= 16 ? 2 : 4;
-  Args a{};
-  a.sf = sfw1;
-  a.gs = gs_w1;
-  a.N = 2 * I;
-  a.K = H;
-  a.xf = base + L.xf;
-  a.exps = i32(L.xexp);
+  StreamArgs a{};
+  a.split = P.l1;
   a.k = k;
   a.plan = plan;
-  a.n_plan = i32(L.n_plan);
-  a.order = i32(L.order);
-  a.out = f32(L.h);
+  a.n_plan = i32(P.n_plan);
+  a.order = i32(P.order);
+  a.part = reinterpret_cast<float*>(base + P.part);
   a.status = dev_status;
-  const int blocks1 = 2 * I / 128;
-  a.splits = pick_splits((int64_t)blocks1 * busy, H, 4);  // a CTA keeps 32 rows: gate and up
-  st = launch_nt<FFN_L1>(nt, w1, (int64_t)E * 2 * I, a, dim3(blocks1 * a.splits, busy), s);
+  st = launch_stream<FFN_L1>(P.nt, w1, (int64_t)E * 2 * I,
+                             Operands{sfw1, gs_w1, 2 * I, H, base + P.xf, i32(P.xexp)}, a, s);
   if (st != NVFP4_OK) return st;
-  st = launch_after(
-      convert_kernel<true>, dim3(S), 256, 0, 1, true, s, "convert_kernel", f32(L.h), (int64_t)I * 4, I,
-      base + L.hf, i32(L.hexp));
+  st = launch(swiglu_kernel, dim3(S), 512, 0, 1, true, s, "swiglu_kernel", a.part, P.l1,
+              i32(P.n_plan), i32(P.slot_unit), I, base + P.hf, i32(P.hexp));
   if (st != NVFP4_OK) return st;
-  a.sf = sfw2;
-  a.gs = gs_w2;
-  a.N = H;
-  a.K = I;
-  a.xf = base + L.hf;
-  a.exps = i32(L.hexp);
-  a.out = f32(L.ys);
-  const int blocks2 = H / 128;
-  a.splits = pick_splits((int64_t)blocks2 * busy, I, kMaxSplits);
-  st = launch_nt<FFN_L2>(nt, w2, (int64_t)E * H, a, dim3(blocks2 * a.splits, busy), s);
+  a.split = P.l2;
+  st = launch_stream<FFN_L2>(P.nt, w2, (int64_t)E * H,
+                             Operands{sfw2, gs_w2, H, I, base + P.hf, i32(P.hexp)}, a, s);
   if (st != NVFP4_OK) return st;
-  return launch_after(
-      combine_slots_kernel, dim3(T, (H / 4 + 255) / 256), 256, 0, 1, true, s, "combine_slots_kernel",
-      f32(L.ys), ids, wts, H, E, k, static_cast<__nv_bfloat16*>(out_bf16));
+  return launch(combine_slots_kernel, dim3(T, H / 128), 32 * kCombineWarps, 0, 1, true, s,
+                "combine_slots_kernel", a.part, P.l2, i32(P.n_plan), i32(P.slot_unit), wts, H, k,
+                static_cast<__nv_bfloat16*>(out_bf16));
 }

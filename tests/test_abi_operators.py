@@ -36,7 +36,7 @@ def test_linear_w4a16_workspace(L):
     (dict(ld=64), 1),                    # ld < K
     (dict(ld=132), 2),                   # ld % 8
     (dict(M=-1), 1),
-    (dict(M=32 * 65535 + 1), 2),
+    (dict(M=16 * 65535 + 1), 2),
     (dict(N=0), 1),
     (dict(out_dtype=2), 1),
     (dict(x=None), 1),
