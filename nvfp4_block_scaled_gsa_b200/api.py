@@ -365,20 +365,26 @@ def _call_on(dev, name, *args):
             call(name, *args, torch._C._cuda_getCurrentRawStream(dev.index))
 
 
-def _same_device(dev, *tensors):
+def _ptrs(dev, *tensors):
+    """Data pointers (None for None) of tensors that all have to be on the CUDA device dev."""
     assert dev.type == "cuda", "CUDA tensors only"
-    index = dev.index
+    index, out = dev.index, []
     for t in tensors:
-        assert t is None or t.get_device() == index, f"all tensors must be on {dev}"
+        if t is None:
+            out.append(None)
+        else:
+            assert t.get_device() == index, f"all tensors must be on {dev}"
+            out.append(t.data_ptr())
+    return out
 
 
-def _check_weights(w: "NVFP4Weights", dev):
-    """The buffers of w as the kernels index them."""
+def _weight_ptrs(w: "NVFP4Weights", dev):
+    """Pointers to the codes, scales and global scales of w, checked as the kernels index them."""
     codes, sf, gs = w.codes, w.sf, w.gs
-    _same_device(dev, codes, sf, gs)
     assert codes.dtype == U8 and codes.is_contiguous() and codes.shape == (w.E * w.N, w.K // 2)
     assert sf.dtype == U8 and sf.is_contiguous() and sf.numel() >= w.E * sf_bytes(w.N, w.K)
     assert gs.dtype == F32 and gs.is_contiguous() and gs.numel() >= w.E
+    return _ptrs(dev, codes, sf, gs)
 
 
 def _bytes(ws):
@@ -406,17 +412,18 @@ def linear_w4a16(x, w: "NVFP4Weights", out_dtype=BF16, out=None, ws=None, status
     M, K = x.shape
     dev = x.device
     assert K == w.K
-    _check_weights(w, dev)
-    _same_device(dev, out, ws, status)
+    weight = _weight_ptrs(w, dev)
     if out is None:
         out = torch.empty(M, w.N, dtype=out_dtype, device=dev)
-    assert out.dtype == out_dtype and out.shape == (M, w.N) and out.is_contiguous()
+    else:
+        assert out.dtype == out_dtype and out.shape == (M, w.N) and out.is_contiguous()
     if ws is None:
         need = linear_w4a16_workspace_bytes(M, w.N, K)
         if need > 0:
             ws = torch.empty(need, dtype=U8, device=dev)
-    _call_on(dev, "nvfp4_linear_w4a16", _p(x), M, K, _row_stride(x), _p(w.codes), _p(w.sf),
-             _p(w.gs), w.N, _p(out), 0 if out_dtype == F32 else 1, _p(ws), _bytes(ws), _p(status))
+    px, pout, pws, pstatus = _ptrs(dev, x, out, ws, status)
+    _call_on(dev, "nvfp4_linear_w4a16", px, M, K, _row_stride(x), *weight, w.N, pout,
+             0 if out_dtype == F32 else 1, pws, _bytes(ws), pstatus)
     return out
 
 
@@ -435,9 +442,7 @@ def moe_ffn_w4a16(x, logits, k, w1: NVFP4Weights, w2: NVFP4Weights, ids=None, we
     E, I = w1.E, w1.N // 2
     assert w2.E == E and w1.K == H and w2.N == H and w2.K == I
     dev = x.device
-    _check_weights(w1, dev)
-    _check_weights(w2, dev)
-    _same_device(dev, logits, ids, weights, out, ws, status)
+    weight1, weight2 = _weight_ptrs(w1, dev), _weight_ptrs(w2, dev)
     if logits is not None:
         assert ids is None and weights is None
         assert logits.dtype == F32 and logits.shape == (T, E) and logits.is_contiguous()
@@ -450,17 +455,17 @@ def moe_ffn_w4a16(x, logits, k, w1: NVFP4Weights, w2: NVFP4Weights, ids=None, we
     if ws is None:
         ws = torch.empty(max(moe_ffn_w4a16_workspace_bytes(T, H, I, E, k), 256), dtype=U8,
                          device=dev)
-    _call_on(dev, "moe_ffn_w4a16", _p(x), _p(logits), _p(ids), _p(weights), T, H, I, E, k,
-             _p(w1.codes), _p(w1.sf), _p(w1.gs), _p(w2.codes), _p(w2.sf), _p(w2.gs), _p(out),
-             _p(ws), _bytes(ws), _p(status))
+    px, plogits, pids, pweights, pout, pws, pstatus = _ptrs(dev, x, logits, ids, weights, out, ws,
+                                                            status)
+    _call_on(dev, "moe_ffn_w4a16", px, plogits, pids, pweights, T, H, I, E, k, *weight1, *weight2,
+             pout, pws, _bytes(ws), pstatus)
     return out
 
 
-def _balance_operands(logits, seq_offs, mask, dloss, dlogits, status):
+def _balance_operands(logits, seq_offs, mask, dloss, dlogits):
     """Checks shared by the balance loss and its gradient; returns (T, E, sequences)."""
     assert logits.dtype == F32 and logits.dim() == 2 and logits.stride(1) == 1
     T, E = logits.shape
-    _same_device(logits.device, seq_offs, mask, dloss, dlogits, status)
     S = 1
     if seq_offs is not None:
         assert seq_offs.dtype == I32 and seq_offs.dim() == 1 and seq_offs.is_contiguous()
@@ -485,9 +490,8 @@ def balance_loss(logits, ids, alpha, seq_offs=None, mask=None, want_grad=False, 
     None).  want_grad: dlogits (T, E) float32, times dloss (device float[1], default 1), in the
     same pass; a given dlogits is added to."""
     accumulate = dlogits is not None
-    T, E, S = _balance_operands(logits, seq_offs, mask, dloss, dlogits, status)
+    T, E, S = _balance_operands(logits, seq_offs, mask, dloss, dlogits)
     dev = logits.device
-    _same_device(dev, ids, ws)
     assert ids.dtype == I32 and ids.dim() == 2 and ids.shape[0] == T and ids.is_contiguous()
     k = ids.shape[1]
     counts = torch.empty(S, E, dtype=I32, device=dev)
@@ -497,9 +501,9 @@ def balance_loss(logits, ids, alpha, seq_offs=None, mask=None, want_grad=False, 
         dlogits = torch.empty(T, E, dtype=F32, device=dev)
     if ws is None:
         ws = torch.empty(int(lib().moe_balance_loss_workspace_size(T, E)), dtype=U8, device=dev)
-    _call_on(dev, "moe_balance_loss", _p(logits), _row_stride(logits), T, E, k, _p(ids),
-             _p(seq_offs), S, _p(mask), float(alpha), _p(counts), _p(tokens), _p(loss), _p(dloss),
-             _p(dlogits), int(accumulate), _p(ws), _bytes(ws), _p(status))
+    p = _ptrs(dev, logits, ids, seq_offs, mask, counts, tokens, loss, dloss, dlogits, ws, status)
+    _call_on(dev, "moe_balance_loss", p[0], _row_stride(logits), T, E, k, p[1], p[2], S, p[3],
+             float(alpha), p[4], p[5], p[6], p[7], p[8], int(accumulate), p[9], _bytes(ws), p[10])
     return loss, counts, tokens, dlogits
 
 
@@ -508,16 +512,15 @@ def balance_loss_backward(logits, counts, tokens, k, alpha, dloss=None, seq_offs
     """The gradient of balance_loss with respect to the logits, from its counts and tokens: float32
     (T, E), times dloss (device float[1], default 1).  A given dlogits is added to."""
     accumulate = dlogits is not None
-    T, E, S = _balance_operands(logits, seq_offs, mask, dloss, dlogits, None)
+    T, E, S = _balance_operands(logits, seq_offs, mask, dloss, dlogits)
     dev = logits.device
-    _same_device(dev, counts, tokens)
     assert counts.dtype == I32 and counts.shape == (S, E) and counts.is_contiguous()
     assert tokens.dtype == I32 and tokens.shape == (S,) and tokens.is_contiguous()
     if dlogits is None:
         dlogits = torch.empty(T, E, dtype=F32, device=dev)
-    _call_on(dev, "moe_balance_loss_backward", _p(logits), _row_stride(logits), T, E, k,
-             _p(counts), _p(tokens), _p(seq_offs), S, _p(mask), float(alpha), _p(dloss),
-             _p(dlogits), int(accumulate))
+    p = _ptrs(dev, logits, counts, tokens, seq_offs, mask, dloss, dlogits)
+    _call_on(dev, "moe_balance_loss_backward", p[0], _row_stride(logits), T, E, k, p[1], p[2], p[3],
+             S, p[4], float(alpha), p[5], p[6], int(accumulate))
     return dlogits
 
 
@@ -525,7 +528,6 @@ def _norm_operands(r, y, post_gamma, gate, pre_gamma):
     """Checks shared by residual_norm and its gradient; returns (T, H, gate kind)."""
     assert r.dtype in (BF16, F32) and r.dim() == 2 and r.stride(1) == 1
     T, H = r.shape
-    _same_device(r.device, y, post_gamma, gate, pre_gamma)
     if y is not None:
         assert y.dtype == BF16 and y.shape == (T, H) and y.stride(1) == 1
     for g in (post_gamma, pre_gamma):
@@ -552,7 +554,6 @@ def residual_norm(r, y, post_gamma=None, gate=None, scale=1.0, pre_gamma=None, e
     float32 (or None) for residual_norm_backward."""
     T, H, kind = _norm_operands(r, y, post_gamma, gate, pre_gamma)
     dev = r.device
-    _same_device(dev, out_r, out_n)
     if y is None:
         assert out_r is None
         out_r = r
@@ -567,10 +568,10 @@ def residual_norm(r, y, post_gamma=None, gate=None, scale=1.0, pre_gamma=None, e
         if out_n is None:
             out_n = torch.empty(T, H, dtype=BF16, device=dev)
         assert out_n.dtype == BF16 and out_n.shape == (T, H) and out_n.is_contiguous()
-    _call_on(dev, "nvfp4_residual_norm", _p(r), 0 if r.dtype == F32 else 1, _row_stride(r), _p(y),
-             H if y is None else _row_stride(y), T, H, _p(post_gamma), _p(gate), kind,
-             float(scale), _p(pre_gamma), float(eps), _p(out_r), _p(out_n), _p(rstd_post),
-             _p(rstd_pre))
+    p = _ptrs(dev, r, y, post_gamma, gate, pre_gamma, out_r, out_n, rstd_post, rstd_pre)
+    _call_on(dev, "nvfp4_residual_norm", p[0], 0 if r.dtype == F32 else 1, _row_stride(r), p[1],
+             H if y is None else _row_stride(y), T, H, p[2], p[3], kind, float(scale), p[4],
+             float(eps), p[5], p[6], p[7], p[8])
     return out_r, out_n, rstd_post, rstd_pre
 
 
@@ -582,7 +583,6 @@ def residual_norm_backward(dr_new, dn, r, y, rstd_post, rstd_pre, post_gamma=Non
     shape: float32 per channel or token, bf16 (T, H)); None where there is no such input."""
     T, H, kind = _norm_operands(r, y, post_gamma, gate, pre_gamma)
     dev = r.device
-    _same_device(dev, dr_new, dn, rstd_post, rstd_pre, ws, status)
     if dr_new is not None:
         assert dr_new.dtype == r.dtype and dr_new.shape == (T, H) and dr_new.is_contiguous()
     if dn is not None:
@@ -602,11 +602,11 @@ def residual_norm_backward(dr_new, dn, r, y, rstd_post, rstd_pre, post_gamma=Non
     if ws is None:
         ws = torch.empty(int(lib().nvfp4_residual_norm_backward_workspace_size(T, H)), dtype=U8,
                          device=dev)
-    _call_on(dev, "nvfp4_residual_norm_backward", _p(dr_new), _p(dn), _p(r),
-             0 if r.dtype == F32 else 1, _row_stride(r), _p(y), H if y is None else _row_stride(y),
-             T, H, _p(post_gamma), _p(gate), kind, float(scale), _p(pre_gamma), _p(rstd_post),
-             _p(rstd_pre), _p(dr), _p(dy), _p(dpost), _p(dpre), _p(dgate), _p(ws), _bytes(ws),
-             _p(status))
+    p = _ptrs(dev, dr_new, dn, r, y, post_gamma, gate, pre_gamma, rstd_post, rstd_pre, dr, dy, dpost,
+              dpre, dgate, ws, status)
+    _call_on(dev, "nvfp4_residual_norm_backward", p[0], p[1], p[2], 0 if r.dtype == F32 else 1,
+             _row_stride(r), p[3], H if y is None else _row_stride(y), T, H, p[4], p[5], kind,
+             float(scale), p[6], p[7], p[8], p[9], p[10], p[11], p[12], p[13], p[14], _bytes(ws), p[15])
     return dict(dr=dr, dy=dy, dpost_gamma=dpost, dpre_gamma=dpre, dgate=dgate)
 
 
