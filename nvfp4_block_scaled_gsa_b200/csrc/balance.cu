@@ -428,7 +428,7 @@ extern "C" nvfp4_status_t moe_balance_loss(const float* logits, int64_t ld, int 
   nvfp4_status_t st = check_shape(T, E, k, ld, S, seq_offs);
   if (st != NVFP4_OK) return st;
   if (!counts || !tokens || !loss || !ws) return NVFP4_ERR_INVALID_ARG;
-  if (T > 0 && (!logits || !topk_ids)) return NVFP4_ERR_INVALID_ARG;
+  if (T > 0 && (!logits || !topk_ids || logits == dlogits)) return NVFP4_ERR_INVALID_ARG;
   if (ws_bytes < moe_balance_loss_workspace_size(T, E)) return NVFP4_ERR_WORKSPACE_TOO_SMALL;
   const void* ptrs4[] = {logits, topk_ids, seq_offs, counts, tokens, loss, dloss, dlogits, dev_status};
   for (const void* p : ptrs4)
@@ -482,7 +482,7 @@ extern "C" nvfp4_status_t moe_balance_loss_backward(const float* logits, int64_t
   const nvfp4_status_t st = check_shape(T, E, k, ld, S, seq_offs);
   if (st != NVFP4_OK) return st;
   if (!counts || !tokens) return NVFP4_ERR_INVALID_ARG;
-  if (T > 0 && (!logits || !dlogits)) return NVFP4_ERR_INVALID_ARG;
+  if (T > 0 && (!logits || !dlogits || logits == dlogits)) return NVFP4_ERR_INVALID_ARG;
   const void* ptrs4[] = {logits, seq_offs, counts, tokens, dloss, dlogits};
   for (const void* p : ptrs4)
     if (reinterpret_cast<uintptr_t>(p) & 3u) return NVFP4_ERR_MISALIGNED;

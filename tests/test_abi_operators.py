@@ -11,6 +11,7 @@ from nvfp4_block_scaled_gsa_b200 import build as B
 from nvfp4_block_scaled_gsa_b200 import _native as N
 
 F = ctypes.c_void_p(1 << 20)         # never dereferenced: every call below fails host validation
+G = ctypes.c_void_p(1 << 21)         # another such
 ODD = ctypes.c_void_p((1 << 20) + 8)  # 4- but not 16-byte aligned
 BAD4 = ctypes.c_void_p((1 << 20) + 2)
 BIG = 1 << 40
@@ -25,9 +26,11 @@ def L():
 def test_linear_w4a16_workspace(L):
     ws = L.nvfp4_linear_w4a16_workspace_size
     assert ws(1, 4096, 7168) == 0                       # a few rows: none
-    # 16 rows of 28 steps of 512 bytes and one word per row, in 256-byte units
-    assert ws(16, 4096, 7168) == 16 * 28 * 512 + 256
-    assert ws(100, 64, 64) == 100 * 512 + 512           # K rounded up to a whole step
+    # 16 rows of 28 steps of 576 bytes and one word per row, in 256-byte units
+    assert ws(16, 4096, 7168) == 16 * 28 * 576 + 256
+    assert ws(100, 64, 64) == 112 * 576 + 512           # rows in blocks of 16, K in whole steps
+    # many output blocks: also float32 planes, 4 for each row (2 pieces of 2 K warps)
+    assert ws(5, 65521, 7168) == 8 * 28 * 576 + 256 + 5 * 4 * 512 * 128 * 4
     assert ws(0, 64, 64) == 0 and ws(-1, 64, 64) == 0 and ws(4, 0, 64) == 0
 
 
@@ -113,6 +116,7 @@ def test_moe_ffn_w4a16_workspace(L):
     (dict(counts=None), 1),
     (dict(tokens=None), 1),
     (dict(loss=None), 1),
+    (dict(dlogits=F), 1),                # in place of the logits
     (dict(ws=None), 1),
     (dict(ws_bytes=8), 4),
     (dict(logits=BAD4), 3),
@@ -135,12 +139,13 @@ def test_balance_loss_refusals(L, change, code):
     (dict(counts=None), 1),
     (dict(tokens=None), 1),
     (dict(dlogits=None), 1),
+    (dict(dlogits=F), 1),                # in place of the logits
     (dict(dloss=BAD4), 3),
     (dict(T=0, logits=None, dlogits=None), 0),
 ])
 def test_balance_loss_backward_refusals(L, change, code):
     a = dict(logits=F, ld=8, T=16, E=8, k=2, counts=F, tokens=F, offs=None, S=1, mask=None,
-             alpha=0.01, dloss=None, dlogits=F, acc=0, stream=None)
+             alpha=0.01, dloss=None, dlogits=G, acc=0, stream=None)
     a.update(change)
     assert L.moe_balance_loss_backward(*a.values()) == code
 

@@ -72,3 +72,36 @@ def test_block_forward_and_back(T):
     W.check(out, *P.linear(n.double().cpu().numpy(), headf))
     N.check_backward(b, back, r2, n, 0.5, N.EPS)
     N.check_backward(dict(a, y=None, gate=None, post_gamma=None), first, back["dr"], x, 1.0, N.EPS)
+
+
+def test_calls_on_two_streams_at_once():
+    """Two streams, each with its own inputs and workspaces, many calls in flight: the results of
+    either are those of the calls alone."""
+    T, H, I, E, k = 6, 256, 128, 8, 2
+    w1, w2, _, _ = W.make_experts(E, H, I, seed=31)
+    head, _ = W.make_weight(20000, H, seed=32)
+    runs = []
+    for seed in (33, 34):
+        a = N.make(T, H, torch.bfloat16, "channel", True, True, seed)
+        lg = torch.randn(T, E, generator=torch.Generator().manual_seed(seed)).to(DEV)
+
+        def step(a=a, lg=lg):
+            x = nv.residual_norm(a["r"], a["y"], a["post_gamma"], a["gate"], 1.0, a["pre_gamma"])
+            y = nv.moe_ffn_w4a16(x[1], lg, k, w1, w2)
+            d = nv.residual_norm_backward(x[0], y, a["r"], a["y"], x[2], x[3], a["post_gamma"],
+                                          a["gate"], 1.0, a["pre_gamma"])
+            ids = nv.permute(lg, k)["ids"]
+            return [y, nv.linear_w4a16(y, head), d["dy"], d["dpost_gamma"],
+                    *nv.balance_loss(lg, ids, 0.1, want_grad=True)]
+        runs.append((step, step(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, (step, _, s) in enumerate(runs):
+            with torch.cuda.stream(s):
+                got[i].append(step())
+    torch.cuda.synchronize()
+    for i, (_, want, _) in enumerate(runs):
+        for g in got[i]:
+            for u, v in zip(g, want):
+                assert torch.equal(u, v)

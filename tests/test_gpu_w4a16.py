@@ -201,6 +201,8 @@ def check_ffn(got, x, ids, wts, f1, f2):
     (16, 256, 128, 4, 2),      # 8 tokens an expert: two token tiles
     (40, 128, 128, 2, 2),      # 40 tokens an expert: blocks of 32
     (33, 256, 64, 40, 6),
+    (60, 128, 1152, 3, 2),     # shares that end inside a block, several units of an expert
+    (3, 4096, 64, 6, 2),       # a long first product in short shares
 ])
 def test_ffn_from_logits_and_from_its_routing(T, H, I, E, k):
     w1, w2, f1, f2 = make_experts(E, H, I, seed=T + E)
@@ -240,6 +242,9 @@ def test_ffn_routing_corner_cases(E):
     nothing = nv.moe_ffn_w4a16(x.to(DEV), None, k, w1, w2, ids=to_dev(np.full((T, k), -1, np.int32)),
                                weights=to_dev(wts))
     assert (nothing == 0).all()
+    empty = nv.moe_ffn_w4a16(x.to(DEV)[:0], None, k, w1, w2, ids=to_dev(base[:0]),
+                             weights=to_dev(wts[:0]))
+    assert empty.shape == (0, H)
 
 
 def test_ffn_reports_and_drops_ids_out_of_range():
