@@ -19,10 +19,10 @@
 // would double the MMAs, and they would be the bound).  Infinities and NaNs pass through the
 // conversion and the product as such.
 //
-// Layout.  A warp owns 32 rows of a 128-row block, rows 8*rg + g + 32*i (g = lane/4, i < 4), and
-// per step 256 elements of K, lane q = lane%4 the 64 elements from 64*q: 32 bytes of codes per
-// row and one 16-byte line of a scale atom, which holds the scales of exactly those 4 rows and
-// 64 elements.  The order of K inside a step is free as long as both operands agree, so a lane's
+// Layout.  A warp owns 16 or 32 rows of a 128-row block, of which a lane's (g = lane/4) are 32 apart,
+// and per step 256 elements of K, lane q = lane%4 the 64 elements from 64*q: 32 bytes of codes per
+// row, and 4 bytes per row of one 16-byte line of a scale atom, which holds the scales of 4 rows 32
+// apart and 64 elements.  The order of K inside a step is free as long as both operands agree, so a lane's
 // own 4 weights of a row are the 4 K positions the MMA wants from it, and the converted
 // activations are stored in that order.
 #include <cuda_fp16.h>
@@ -36,9 +36,7 @@
 namespace nvfp4 {
 namespace {
 
-constexpr int kRowWarps = 4;               // 4 x 32 rows = one 128-row scale atom
-constexpr int kKWarps = 2;                 // warps that share a row group, taking steps in turn
-constexpr int kConsumers = kRowWarps * kKWarps;
+constexpr int kConsumers = 8;              // warps that multiply
 constexpr int kThreads = 32 * (kConsumers + 1);  // and one warp that issues the copies
 constexpr int kStepK = 256;                // elements of K per step
 constexpr int kStepX = kStepK * 2;         // bytes of a token's converted activations per step
@@ -54,15 +52,27 @@ constexpr int kRedStride = 128 + 4;
 // with a converting kernel in front; with 28 pieces (1 x 65536 x 7168, 512 CTAs) 58 against 55.
 constexpr int kMaxPieces = 2 * kConsumers;
 
+// How the 8 warps share a step's 128 rows.  With one token tile (NT = 1) a warp owns 32 rows and two
+// warps take the steps in turn: few instructions per weight go to waiting and to the activations
+// (16 tokens of 256 experts: 374 us, against 415 with 16 rows a warp).  With two tiles the MMAs
+// weigh more and a warp owns 16 rows of every step, which frees the stages sooner and halves the
+// accumulators (16 x 65536 x 4096: 47 us, against 54).
+template <int NT>
+struct Warps {
+  static constexpr int KW = NT == 1 ? 2 : 1;  // warps that share rows, taking steps in turn
+  static constexpr int P = KW;                // 16-row tiles of a warp
+};
+
 template <int NT, bool XIN>
 struct Cfg {
   static constexpr int TOK = 8 * NT;  // token columns
+  static constexpr int KW = Warps<NT>::KW;
   static constexpr int STAGE = kWTile + kSTile + (XIN ? 0 : (TOK * kXRow + 1023) / 1024 * 1024);
   static constexpr int STAGES = 4;
   static constexpr int X_AT = STAGES * STAGE;  // XIN: the activations behind the stages
   static constexpr int SMEM = X_AT + (XIN ? kMaxPieces * kXRow : 0) + 1024;
-  static_assert(kKWarps * TOK * kRedStride * 4 <= STAGES * STAGE, "partial sums reuse the stages");
-  static_assert(STAGES % kKWarps == 0, "a stage is always the same K warps', or one could wait two phases ahead");
+  static_assert(KW * TOK * kRedStride * 4 <= STAGES * STAGE, "partial sums reuse the stages");
+  static_assert(STAGES % KW == 0, "a stage is always the same warps', or one could wait two phases ahead");
   // two CTAs per SM, so that one's start and end overlap the other's stream
   static_assert(2 * (SMEM + 3072) <= 227 * 1024, "shared memory of an SM");
 };
@@ -352,46 +362,58 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(
 
 // ------------------------------------------------------------------------- the product
 
-// What a lane reads of a stage, and the products of one step: 8 words of 8 codes per row.  The sums
-// of a step start from zero and are added to the running sums in plain float32 (the MMA truncates
-// as it accumulates, and over a long K that would drift).
+// What a lane reads of a stage, and the products of one step: 8 words of 8 codes per row, rows `line`
+// + 64 * tile + {0, 32} of the 128.  The sums of a step start from zero and are added to the running
+// sums in plain float32 (the MMA truncates as it accumulates, and over a long K that would drift).
 template <int NT>
 struct Lane {
-  int code_off, piece[2], scale_off, q;
-  __device__ __forceinline__ Lane(int rg, int lane) {
-    const int g = lane >> 2;
+  static constexpr int P = Warps<NT>::P, KW = Warps<NT>::KW;
+  using Acc = float[P][NT][4];
+  int line, tile0, wk, q;  // wk: which of the KW warps of these rows this is
+  int code_off, piece[2], scale_off;
+  __device__ __forceinline__ Lane(int warp, int lane) {
+    const int g = lane >> 2, high = warp >> 2;
+    line = 8 * (warp & 3) + g;
+    tile0 = KW == 1 ? high : 0;
+    wk = KW == 1 ? 0 : high;
     q = lane & 3;
     // two 16-byte pieces of a row's 128 bytes (128-byte swizzle: the piece index is xored with the
     // row's index modulo 8, which is g for all of the lane's rows)
-    code_off = (8 * rg + g) * 128;
+    code_off = (line + 64 * tile0) * 128;
     piece[0] = ((2 * q) ^ g) * 16;
     piece[1] = ((2 * q + 1) ^ g) * 16;
-    scale_off = kWTile + q * 512 + (8 * rg + g) * 16;
+    scale_off = kWTile + q * 512 + line * 16 + 8 * tile0;
   }
+  __device__ __forceinline__ int row(int p, int r) const { return line + 64 * (tile0 + p) + 32 * r; }
   // left: elements of K from the step's first one on (the last step may hold fewer than 256)
   __device__ __forceinline__ void step(const uint8_t* st, const uint8_t* const (&xb)[NT], int left,
-                                       float (&acc)[2][NT][4]) const {
-    // with one token tile each row pair has two accumulators, so that a warp's consecutive MMAs do
-    // not wait for one another
-    constexpr int CH = NT == 1 ? 2 : 1;
-    uint32_t sc[4][2];
+                                       Acc& acc) const {
+    // two accumulators where a warp has few, so that consecutive MMAs do not wait for one another
+    constexpr int CH = P * NT == 4 ? 1 : 2;
+    uint32_t sc[2 * P][2];
     {
-      uint4 sv = lds16(st + scale_off);
+      uint4 sv;
+      if constexpr (P == 2) {
+        sv = lds16(st + scale_off);
+      } else {
+        const uint2 two = *reinterpret_cast<const uint2*>(st + scale_off);
+        sv = make_uint4(two.x, two.y, 0u, 0u);
+      }
       // past K the codes are zeros, but the scale bytes are whatever was there
       if (q * 64 >= left) sv = make_uint4(0u, 0u, 0u, 0u);
       const uint32_t sw[4] = {sv.x, sv.y, sv.z, sv.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 2 * P; ++j) {
         sc[j][0] = decode_scales(sw[j] & 0xFFFFu);
         sc[j][1] = decode_scales(sw[j] >> 16);
       }
     }
-    float tmp[CH][2][NT][4];
+    float tmp[CH][P][NT][4];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      uint32_t w[4][4];
+      uint32_t w[2 * P][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 2 * P; ++j) {
         const uint4 v = lds16(st + code_off + j * (32 * 128) + piece[half]);
         w[j][0] = v.x;
         w[j][1] = v.y;
@@ -404,7 +426,7 @@ struct Lane {
 #pragma unroll
         for (int n = 0; n < NT; ++n) b[n] = lds16(xb[n] + half * 256 + wd * 64);
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
+        for (int p = 0; p < P; ++p) {
           uint32_t a[2][4];
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
@@ -434,7 +456,7 @@ struct Lane {
       }
     }
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
+    for (int p = 0; p < P; ++p)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -443,17 +465,15 @@ struct Lane {
           if (CH == 2) acc[p][n][j] += tmp[CH - 1][p][n][j];
         }
   }
+  static __device__ __forceinline__ void clear(Acc& acc) {
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[p][n][j] = 0.0f;
+  }
 };
-
-template <int NT>
-__device__ __forceinline__ void clear(float (&acc)[2][NT][4]) {
-#pragma unroll
-  for (int p = 0; p < 2; ++p)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[p][n][j] = 0.0f;
-}
 
 // The global scale (a positive normal number) as 2^exp * frac, and a sum times 2^-row_exp / 2^exp in
 // two exact steps; dividing by frac is left.
@@ -473,7 +493,7 @@ struct GlobalScale {
 };
 
 // The stage ring: the barriers, and the copies of a step's codes and scales.
-template <int STAGES>
+template <int STAGES, int KW>
 struct Ring {
   uint64_t *full, *empty;
   volatile int* abort_flag;
@@ -481,7 +501,7 @@ struct Ring {
     *abort_flag = 0;
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(smem_u32(&full[i]), 1);
-      mbar_init(smem_u32(&empty[i]), kRowWarps);
+      mbar_init(smem_u32(&empty[i]), kConsumers / KW);
     }
     fence_mbar_init();
   }
@@ -562,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   __shared__ __align__(16) uint8_t zeros[kStepX];  // what columns without a token read
   __shared__ int s_exp[TOK];                       // power of two of each column
   __shared__ uint32_t s_amax[TOK];                 // XIN
-  const Ring<STAGES> ring{bar_full, bar_empty, &abort_flag};
+  const Ring<STAGES, C::KW> ring{bar_full, bar_empty, &abort_flag};
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, q = lane & 3;
   const int split = static_cast<int>(blockIdx.x) % A.splits;
@@ -575,8 +595,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int st0 = static_cast<int>((int64_t)nsteps * split / A.splits);
   const int n_st = static_cast<int>((int64_t)nsteps * (split + 1) / A.splits) - st0;
   const GlobalScale gs(__ldg(W.gs));
-  float acc[2][NT][4];
-  clear<NT>(acc);
+  const Lane<NT> me(warp & 7, lane);
+  typename Lane<NT>::Acc acc;
+  me.clear(acc);
   if (warp == kConsumers) {
     const uint8_t* sf = W.sf + (int64_t)rowblk * atoms_k * 512;
     auto stage = [&](int i) { return smem + (i % STAGES) * C::STAGE; };
@@ -601,8 +622,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (!ok) ring.drain(issued);
   } else {
-    const int rg = warp % kRowWarps, wk = warp / kRowWarps;
-    const Lane<NT> me(rg, lane);
     if constexpr (XIN) {
       // pieces (token, step) warp and warp + kConsumers: lane l holds elements 8l .. 8l + 7
       const int pieces = ntok * n_st;
@@ -642,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       pdl_wait();
       s_exp[tid] = ld_after(W.exps + m0 + tid);
     }
-    for (int i = wk; i < n_st; i += kKWarps) {
+    for (int i = me.wk; i < n_st; i += C::KW) {
       if (!ring.wait_full(i)) break;
       const uint8_t* st = smem + (i % STAGES) * C::STAGE;
       const uint8_t* xb[NT];
@@ -657,11 +676,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
 
-  // partial sums of the K warps and of the cluster's CTAs -> shared memory, added in order
+  // partial sums of the warps and of the cluster's CTAs -> shared memory, added in order
   __syncthreads();
-  float* red = reinterpret_cast<float*>(smem);  // [kKWarps][TOK][kRedStride]
+  float* red = reinterpret_cast<float*>(smem);  // [KW][TOK][kRedStride]
   if (warp < kConsumers) {
-    const int rg = warp % kRowWarps, wk = warp / kRowWarps;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -671,11 +689,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         float f0, f1;
         gs.factors(s_exp[t], f0, f1);
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
+        for (int p = 0; p < me.P; ++p)
 #pragma unroll
           for (int r = 0; r < 2; ++r)
-            red[(wk * TOK + t) * kRedStride + 8 * rg + g + 64 * p + 32 * r] =
-                acc[p][n][2 * r + c] * f0 * f1;
+            red[(me.wk * TOK + t) * kRedStride + me.row(p, r)] = acc[p][n][2 * r + c] * f0 * f1;
       }
   }
   if (A.splits > 1) cluster_sync();
@@ -688,11 +705,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       float v = 0.0f;
       if (A.splits > 1) {
         const uint32_t a = smem_u32(at);
-        float part[kMaxSplits][kKWarps];
+        float part[kMaxSplits][C::KW];
 #pragma unroll
         for (int c = 0; c < kMaxSplits; ++c)
 #pragma unroll
-          for (int w = 0; w < kKWarps; ++w) {
+          for (int w = 0; w < C::KW; ++w) {
             part[c][w] = 0.0f;
             if (c < A.splits)
               part[c][w] = ld_cluster_f32(mapa_shared(a + w * TOK * kRedStride * 4, c));
@@ -700,10 +717,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int c = 0; c < kMaxSplits; ++c)
 #pragma unroll
-          for (int w = 0; w < kKWarps; ++w) v += part[c][w];
+          for (int w = 0; w < C::KW; ++w) v += part[c][w];
       } else {
 #pragma unroll
-        for (int w = 0; w < kKWarps; ++w) v += at[w * TOK * kRedStride];
+        for (int w = 0; w < C::KW; ++w) v += at[w * TOK * kRedStride];
       }
       v /= gs.frac;
       if (n < W.N) {
@@ -721,10 +738,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 // For many output blocks: the blocks (a unit of up to 8 * NT tokens against 128 weight rows) follow
 // one another, each ceil(K / 256) steps long, and every CTA takes the same number of consecutive
-// steps, wherever its share starts and ends.  A CTA's copies run on across blocks.  What a K warp
+// steps, wherever its share starts and ends.  A CTA's copies run on across blocks.  What a warp
 // sums of a block goes to a plane of its own: `part` holds [row][planes][blocks * 128], plane
-// 2 * piece + K warp, a block's pieces counted from the CTA that starts it.  The kernel behind
-// adds a block's planes in order.
+// KW * piece + wk, a block's pieces counted from the CTA that starts it.  The kernel behind adds
+// a block's planes in order.
 enum Mode { DENSE = 0, FFN_L1 = 1, FFN_L2 = 2 };
 constexpr int kStreamCtas = 2 * 148;  // two per SM, all resident at once
 
@@ -732,6 +749,7 @@ struct Split {
   int blocks;   // of 128 weight rows
   int steps;    // of a block
   int planes;   // of a row, at most
+  int kw;       // of them per piece
   int least;    // steps of a CTA
   int units;    // DENSE; the FFN's are counted on the device
   // (the host sees to it that the steps of all blocks fit 31 bits)
@@ -743,7 +761,7 @@ struct Split {
 };
 // planes that hold something of block b
 __device__ __forceinline__ int block_planes(const Split& S, int per, int b) {
-  return kKWarps * (((b + 1) * S.steps - 1) / per - b * S.steps / per + 1);
+  return S.kw * (((b + 1) * S.steps - 1) / per - b * S.steps / per + 1);
 }
 
 struct StreamArgs {
@@ -767,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   __shared__ __align__(8) uint64_t bar_full[STAGES], bar_empty[STAGES];
   __shared__ volatile int abort_flag;
   __shared__ __align__(16) uint8_t zeros[kStepX];  // what columns without a token read
-  const Ring<STAGES> ring{bar_full, bar_empty, &abort_flag};
+  const Ring<STAGES, C::KW> ring{bar_full, bar_empty, &abort_flag};
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, q = lane & 3;
   if (tid == 0) ring.init();
@@ -872,8 +890,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (!ok) ring.drain(i);
   } else {
     // =========================== products ===========================
-    const int rg = warp % kRowWarps, wk = warp / kRowWarps;
-    const Lane<NT> me(rg, lane);
+    const Lane<NT> me(warp, lane);
     const int64_t n_pad = (int64_t)S.blocks * 128;
     pdl_wait();
     bool ok = true;
@@ -891,9 +908,10 @@ __global__ void __launch_bounds__(kThreads, 2)
           row[t8][c] = t < k.count ? out_row(k, t) : -1;
           row_exp[t8][c] = row[t8][c] >= 0 ? ld_after(W.exps + x_row(row[t8][c])) : 0;
         }
-      float acc[2][NT][4];
-      clear<NT>(acc);
-      for (int i = (it + wk) & 1; i < len; i += kKWarps) {  // the stages it + i with (it + i) % 2 == wk
+      typename Lane<NT>::Acc acc;
+      me.clear(acc);
+      // the stages it + i with (it + i) % KW == wk
+      for (int i = (it + me.wk) & (C::KW - 1); i < len; i += C::KW) {
         if (!ring.wait_full(it + i)) {
           ok = false;
           break;
@@ -908,7 +926,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       it += len;
       const GlobalScale gs(gs_value);
-      const int plane = (static_cast<int>(blockIdx.x) - b * S.steps / per) * kKWarps + wk;
+      const int plane = (static_cast<int>(blockIdx.x) - b * S.steps / per) * C::KW + me.wk;
 #pragma unroll
       for (int t8 = 0; t8 < NT; ++t8)
 #pragma unroll
@@ -916,13 +934,12 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (row[t8][c] < 0) continue;
           float f0, f1;
           gs.factors(row_exp[t8][c], f0, f1);
-          float* d = A.part + ((int64_t)row[t8][c] * S.planes + plane) * n_pad + k.rowblk * 128 +
-                     8 * rg + g;
+          float* d = A.part + ((int64_t)row[t8][c] * S.planes + plane) * n_pad + k.rowblk * 128;
 #pragma unroll
-          for (int p = 0; p < 2; ++p)
+          for (int p = 0; p < me.P; ++p)
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-              d[64 * p + 32 * r] = acc[p][t8][2 * r + c] * f0 * f1 / gs.frac;
+              d[me.row(p, r)] = acc[p][t8][2 * r + c] * f0 * f1 / gs.frac;
         }
     }
   }
@@ -1055,12 +1072,11 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_slots_kernel(
 
 constexpr int kSizingSms = 148;  // the SM count the K splits are sized for
 
-// CTAs along K for one output block: enough CTAs for every SM, while each K warp keeps at least one
-// step.
+// CTAs along K for one output block: enough CTAs for every SM, while each keeps at least two steps.
 int pick_splits(int64_t blocks, int K, int most) {
   const int steps = (K + kStepK - 1) / kStepK;
   int s = 1;
-  while (s < most && blocks * s < kSizingSms && steps / (2 * s) >= kKWarps) s *= 2;
+  while (s < most && blocks * s < kSizingSms && steps / (2 * s) >= 2) s *= 2;
   return s;
 }
 
@@ -1145,14 +1161,15 @@ int64_t converted_bytes(int64_t rows, int K) {
 }
 
 // Shares of at least `least` steps.
-Split make_split(int N, int K, int64_t least, int units) {
+Split make_split(int nt, int N, int K, int64_t least, int units) {
   Split S{};
   S.blocks = static_cast<int>(((int64_t)N + 127) / 128);
   S.steps = (K + kStepK - 1) / kStepK;
   S.least = static_cast<int>(least);
   S.units = units;
   // shares of at least `least` steps that a block of S.steps can lie in
-  S.planes = kKWarps * (S.steps == 1 ? 1 : (S.steps - 2) / S.least + 2);
+  S.kw = nt == 1 ? Warps<1>::KW : Warps<2>::KW;
+  S.planes = S.kw * (S.steps == 1 ? 1 : (S.steps - 2) / S.least + 2);
   return S;
 }
 
@@ -1183,7 +1200,7 @@ LinearW4Plan linear_w4_plan(int64_t M, int N, int K) {
              total <= INT32_MAX;
   if (P.stream) {
     // every CTA's share is known here, so `least` is the share itself
-    P.split = make_split(N, K, (total + kStreamCtas - 1) / kStreamCtas, static_cast<int>(P.tblks));
+    P.split = make_split(P.nt, N, K, (total + kStreamCtas - 1) / kStreamCtas, static_cast<int>(P.tblks));
   } else {
     P.splits = pick_splits(P.rowblks * P.tblks, K, kMaxSplits);
     P.xin = P.nt == 1 && M * ((steps + P.splits - 1) / P.splits) <= kMaxPieces;
@@ -1213,7 +1230,7 @@ FfnW4Plan ffn_w4_plan(int T, int H, int I, int E, int k) {
   // every CTA; with more, whole blocks (2 pieces at most), which keeps the planes small.
   auto split = [&](int N, int K) {
     const int steps = (K + kStepK - 1) / kStepK;
-    return make_split(N, K, S <= 64 && steps > 4 ? 4 : steps, 0);
+    return make_split(P.nt, N, K, S <= 64 && steps > 4 ? 4 : steps, 0);
   };
   P.l1 = split(2 * I, H);
   P.l2 = split(H, I);
