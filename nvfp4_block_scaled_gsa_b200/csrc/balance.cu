@@ -130,6 +130,19 @@ __device__ __forceinline__ int32_t ld_after(const int32_t* p) {
   return v;
 }
 
+// e^x (2^(x log2 e), results below 2^-126 to zero) and 1/x, by the hardware's approximations: relative
+// errors about (2 + 1.4 |x|) 2^-24 and 2^-23.
+__device__ __forceinline__ float exp_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // L lanes per token, 4 * NV logits each; a warp takes 32 / L consecutive tokens at a time.  Many
 // logits per lane keep the shuffles of the row sums few (40961 x 160 at 32 lanes of 8 was bound by
 // instruction issue, 297 a token: 18.4 us against 17.2).  VEC: a lane's logits are NV 16-byte
@@ -257,9 +270,7 @@ __global__ void __launch_bounds__(kThreads, 3) balance_kernel(const Args A) {
     float z = 0.0f, dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) {
-      // ex2.approx of the rounded argument: relative error about (2 + 1.4 |x|) * 2^-24, so at most
-      // 2^-23 of the row's sum of probabilities
-      v[i] = __expf(v[i] - m);
+      v[i] = exp_approx(v[i] - m);  // off by at most 2^-23 of the row's sum of probabilities
       z += v[i];
       dot += v[i] * f[i];
     }
@@ -268,18 +279,19 @@ __global__ void __launch_bounds__(kThreads, 3) balance_kernel(const Args A) {
       z += __shfl_xor_sync(0xffffffffu, z, o);
       dot += __shfl_xor_sync(0xffffffffu, dot, o);
     }
-    const float inv = z == 0.0f ? 0.0f : __frcp_rn(z);
+    const float inv = z == 0.0f ? 0.0f : rcp_approx(z);
     const float vt = dot * inv;
-    if (counted && l == 0) sum += static_cast<double>(coef) * static_cast<double>(vt);
+    if (A.loss != nullptr && counted && l == 0)
+      sum += static_cast<double>(coef) * static_cast<double>(vt);
     if (A.dlogits != nullptr && t < A.T) {
       float* row = A.dlogits + t * E;
       const float scale = up * coef * inv;
       float d[kSlots];
 #pragma unroll
       for (int i = 0; i < kSlots; ++i) d[i] = scale * v[i] * (f[i] - vt);
-      if (!counted) {  // whatever the row holds
+      if (__any_sync(__activemask(), !counted)) {  // (rare, so a branch and not a select each)
 #pragma unroll
-        for (int i = 0; i < kSlots; ++i) d[i] = 0.0f;
+        for (int i = 0; i < kSlots; ++i) d[i] = counted ? d[i] : 0.0f;  // whatever the row holds
       }
       if constexpr (VEC) {
 #pragma unroll
