@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(kCountThreads) balance_count_kernel(
     const int32_t* __restrict__ ids, int T, int E, int k, const int32_t* __restrict__ seq_offs,
     const uint8_t* __restrict__ mask, int cluster, int32_t* __restrict__ counts,
     int32_t* __restrict__ tokens, uint32_t* __restrict__ ticket, int32_t* __restrict__ dev_status) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_trigger();
   __shared__ int hist[kMaxE + 1];  // [E]: the tokens
   const int tid = threadIdx.x;
   const int s = blockIdx.x / cluster, rank = blockIdx.x % cluster;
@@ -126,12 +126,6 @@ struct Args {
   int iters;         // groups of 32 / L tokens per warp
 };
 
-__device__ __forceinline__ int32_t ld_after(const int32_t* p) {
-  int32_t v;
-  asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
-}
-
 // e^x (2^(x log2 e), results below 2^-126 to zero) and 1/x, by the hardware's approximations: relative
 // errors about (2 + 1.4 |x|) 2^-24 and 2^-23.
 __device__ __forceinline__ float exp_approx(float x) {
@@ -191,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 3) balance_kernel(const Args A) {
   }
   if (tid == 0) s_busy = 0;
   __syncthreads();
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the counts
+  pdl_wait();  // the counts
 
   // the last sequence that starts at or before t, given offs[lo] <= t < offs[S]
   auto find = [&](int64_t t, int lo) {
@@ -344,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 3) balance_kernel(const Args A) {
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int c = tid + j * kThreads;
-    if (c < static_cast<int>(gridDim.x)) total += __ldcg(A.part + c);
+    if (c < static_cast<int>(gridDim.x)) total += ld_after(A.part + c);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);

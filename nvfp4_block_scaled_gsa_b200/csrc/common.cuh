@@ -144,6 +144,39 @@ __device__ __forceinline__ void red_add_v4(float* p, float4 v) {
                : "memory");
 }
 
+// ------------------------------------------------------------------------------ dependent launch
+// Programmatic dependent launch: wait until the kernels in front of this one are complete and their
+// writes visible; let the next kernel's CTAs start (they wait in turn).
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+// What a kernel in front wrote is read with these, after pdl_wait(): they are ordered behind it, which
+// the compiler promises neither for loads through const __restrict__ nor for the load intrinsics.
+__device__ __forceinline__ uint4 ld_after16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ int32_t ld_after(const int32_t* p) {
+  int32_t v;
+  asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float ld_after(const float* p) {
+  float v;
+  asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ double ld_after(const double* p) {
+  double v;
+  asm volatile("ld.global.cg.f64 %0, [%1];" : "=d"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // ------------------------------------------------------------------------------ registers
 // Per-warpgroup register budget (setmaxnreg): every thread of a warpgroup executes the same one.
 // An increase waits until other warpgroups have released enough of the registers the block was

@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(MAXT, 1) residual_norm_backward_kernel(const A
     }
     return;
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_trigger();
   if (A.part == nullptr) return;
   float* part = A.part + (int64_t)blockIdx.x * 2 * H;
 #pragma unroll
@@ -522,14 +522,14 @@ __global__ void __launch_bounds__(MAXT, 1) residual_norm_backward_kernel(const A
 // Adds the CTAs' column sums in order (8 interleaved partial sums, then those in order) and makes
 // the gradients of them.  32 columns per CTA; blockIdx.y: 0 = post (and channel gate), 1 = pre.
 __global__ void __launch_bounds__(256) norm_grads_kernel(const Args A, int parts) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_wait();
   __shared__ float s[8][33];
   const int col = blockIdx.x * 32 + threadIdx.x, k = threadIdx.y;
   float v = 0.0f;
   if (col < A.H) {
     const float* p = A.part + (int64_t)blockIdx.y * A.H + col;
 #pragma unroll 8
-    for (int i = k; i < parts; i += 8) v += __ldcg(p + (int64_t)i * 2 * A.H);
+    for (int i = k; i < parts; i += 8) v += ld_after(p + (int64_t)i * 2 * A.H);
   }
   s[k][threadIdx.x] = v;
   __syncthreads();

@@ -81,8 +81,9 @@ struct Cfg {
   static constexpr int SMEM = X_AT + (XIN ? kMaxPieces * kXRow : 0) + 1024;
   static_assert(KW * TOK * kRedStride * 4 <= STAGES * STAGE, "partial sums reuse the stages");
   static_assert(STAGES % KW == 0, "a stage is always the same warps', or one could wait two phases ahead");
-  // two CTAs per SM, so that one's start and end overlap the other's stream
-  static_assert(2 * (SMEM + 3072) <= 227 * 1024, "shared memory of an SM");
+  // two CTAs per SM, so that one's start and end overlap the other's stream (beside the static
+  // shared memory, the system takes 1 KB of each)
+  static_assert(2 * (SMEM + 2560) <= 228 * 1024, "shared memory of an SM");
 };
 
 // A weight tensor and the converted activations it is multiplied with.
@@ -140,13 +141,6 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
-// Programmatic dependent launch: wait until the kernels before this one are complete and visible;
-// let the next kernel's CTAs start (they wait in turn).
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void pdl_trigger() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 // ------------------------------------------------------------------- converted activations
 
 // Exponent e with amax * 2^e in [2^14, 2^15), at most 126 (then every value fits f16 anyway);
@@ -157,22 +151,6 @@ __device__ __forceinline__ int norm_exp(uint32_t amax_bits) {
 }
 __device__ __forceinline__ float pow2f(int e) {  // e in [-126, 127]
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-}
-
-// What an earlier kernel of a dependent launch wrote is read with these, after pdl_wait(): they are
-// ordered behind it, which the compiler does not promise for loads through const __restrict__.
-__device__ __forceinline__ uint4 ld_after16(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p)
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ int32_t ld_after(const int32_t* p) {
-  int32_t v;
-  asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
 }
 
 // float32 bits of the largest finite magnitude of some values
@@ -955,12 +933,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (tid == 0 && abort_flag) report(A.status, NVFP4_DEVERR_TIMEOUT);
 }
 
-// Sums over a block's planes, in order, of V groups of 4 consecutive columns; the loads of 16 / V
-// planes are in flight together.
+// Sums over a block's planes, in order, of V groups of 4 consecutive columns; the loads of 8 planes
+// are in flight together.
 template <int V>
 __device__ __forceinline__ void sum_planes(const float* base, const int (&at)[V], int64_t n_pad,
                                            int planes, float (&v)[V][4]) {
-  constexpr int kAhead = 16 / V;
+  constexpr int kAhead = 8;
 #pragma unroll
   for (int g = 0; g < V; ++g)
 #pragma unroll
@@ -1051,7 +1029,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_slots_kernel(
     float4 wy = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const int unit = j < k ? ld_after(slot_unit + t * k + j) : -1;
     if (unit >= 0) {
-      const float wj = __int_as_float(ld_after(reinterpret_cast<const int32_t*>(w) + t * k + j));
+      const float wj = ld_after(w + t * k + j);
       float y[1][4];
       sum_planes<1>(part + (t * k + j) * S.planes * n_pad, {c}, n_pad,
                     block_planes(S, per, unit * S.blocks + blockIdx.y), y);
