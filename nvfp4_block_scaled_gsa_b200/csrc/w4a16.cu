@@ -255,13 +255,14 @@ __global__ void __launch_bounds__(256) convert_kernel(const uint8_t* x, int64_t 
 // token's activations each.
 constexpr int kPlanThreads = 512;
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(
-    const float* __restrict__ logits, int T, int E, int k, int tok, int32_t* ids, float* w,
-    int4* __restrict__ plan, int32_t* __restrict__ n_plan, int32_t* __restrict__ order,
+    const float* __restrict__ logits, int T, int E, int k, int tok, const int32_t* __restrict__ ids,
+    float* w, int4* __restrict__ plan, int32_t* __restrict__ n_plan, int32_t* __restrict__ order,
     int32_t* __restrict__ slot_unit, const uint8_t* __restrict__ x, int H,
     uint8_t* __restrict__ xf, int32_t* __restrict__ exps, int32_t* __restrict__ dev_status) {
   constexpr int kWarps = kPlanThreads / 32;
   __shared__ int hist[kWarps][kMaxE];
   __shared__ int first_of[kMaxE], unit_of[kMaxE];
+  __shared__ int s_ids[NVFP4_W4A16_MAX_SLOTS];
   __shared__ uint32_t red[32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
@@ -271,14 +272,16 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(
     return;
   }
   for (int i = tid; i < kWarps * kMaxE; i += kPlanThreads) (&hist[0][0])[i] = 0;
-  if (logits != nullptr)
-    for (int t = warp; t < T; t += kWarps) topk_token(logits, t, E, k, 1, lane, ids, w);
-  __syncthreads();  // also: this CTA's ids are visible to all its threads
   const int S = T * k, per = (S + kWarps - 1) / kWarps;
+  if (logits != nullptr)
+    for (int t = warp; t < T; t += kWarps) topk_token(logits, t, E, k, 1, lane, s_ids, w);
+  else
+    for (int s = tid; s < S; s += kPlanThreads) s_ids[s] = __ldg(ids + s);
+  __syncthreads();
   const int lo = min(S, warp * per), hi = min(S, lo + per);
   bool bad = false;
   for (int s = lo + lane; s < hi; s += 32) {
-    const int e = ids[s];
+    const int e = s_ids[s];
     if (e >= E) bad = true;
     else if (e >= 0) atomicAdd(&hist[warp][e], 1);
   }
@@ -329,7 +332,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(
   __syncthreads();
   for (int base = lo; base < hi; base += 32) {
     const int s = base + lane;
-    int e = s < hi ? ids[s] : -1;
+    int e = s < hi ? s_ids[s] : -1;
     if (e >= E) e = -1;
     const unsigned peers = __match_any_sync(0xffffffffu, e);
     const int before = __popc(peers & ((1u << lane) - 1u));
@@ -856,7 +859,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     Cursor early = c;
     enter(early, false);
     const int head = min(n, STAGES);
-    for (int i = 0; i < head; ++i) {  // while the activations are being made
+    // while the activations are being made (bringing more than the ring holds into L2 meanwhile
+    // made one token's FFN slower: 56 us with 8 steps a CTA against 53.5)
+    for (int i = 0; i < head; ++i) {
       copy_w(i, early);
       advance(early, false);
     }
@@ -1204,7 +1209,7 @@ LinearW4Plan linear_w4_plan(int64_t M, int N, int K) {
 struct FfnW4Plan {
   int nt;
   Split l1, l2;
-  int64_t ids, w, plan, n_plan, order, slot_unit, xf, xexp, hf, hexp, part, total;
+  int64_t w, plan, n_plan, order, slot_unit, xf, xexp, hf, hexp, part, total;
 };
 
 FfnW4Plan ffn_w4_plan(int T, int H, int I, int E, int k) {
@@ -1226,7 +1231,6 @@ FfnW4Plan ffn_w4_plan(int T, int H, int I, int E, int k) {
     o = round_up(o + bytes, 256);
     return at;
   };
-  P.ids = take(S * 4);
   P.w = take(S * 4);
   P.plan = take(S * 16);
   P.n_plan = take(4);
@@ -1336,13 +1340,12 @@ extern "C" nvfp4_status_t moe_ffn_w4a16(const void* x_bf16, const float* logits,
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(ws);
   auto i32 = [&](int64_t off) { return reinterpret_cast<int32_t*>(base + off); };
-  int32_t* ids = logits != nullptr ? i32(P.ids) : const_cast<int32_t*>(topk_ids);
   float* wts = logits != nullptr ? reinterpret_cast<float*>(base + P.w) : const_cast<float*>(topk_w);
   int4* plan = reinterpret_cast<int4*>(base + P.plan);
   const int S = T * k;
   nvfp4_status_t st =
       launch(plan_kernel, dim3(1 + T), kPlanThreads, 0, 1, false, s, "plan_kernel", logits, T, E, k,
-             8 * P.nt, ids, wts, plan, i32(P.n_plan), i32(P.order), i32(P.slot_unit),
+             8 * P.nt, topk_ids, wts, plan, i32(P.n_plan), i32(P.order), i32(P.slot_unit),
              static_cast<const uint8_t*>(x_bf16), H, base + P.xf, i32(P.xexp), dev_status);
   if (st != NVFP4_OK) return st;
   StreamArgs a{};
