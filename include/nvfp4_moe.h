@@ -509,8 +509,8 @@ NVFP4_API nvfp4_status_t moe_ffn_forward_ex(const void* x_bf16, const float* log
  * stored weights with bf16 activations: every decoded weight is exact, products are summed in
  * FP32, the result is rounded once.
  *
- *   x         bf16 [M][ld] (ld >= K, ld % 8 == 0), any M >= 0.  Blocks of 32 rows each read the
- *             weights again: meant for up to a few dozen rows
+ *   x         bf16 [M][ld] (ld >= K, ld % 8 == 0).  Every block of 16 rows goes through the weights
+ *             again (out of L2 where they stay there): meant for up to a few dozen rows
  *   w, sfw    NVFP4 [N][K] (codes [N][K/2], tiled scales), gs_w device float[1]
  *   out       [M][N], out_dtype 0 = float32, 1 = bf16:
  *             out[m][n] = sum_k x[m][k] * E2M1(w[n][k]) * E4M3(sfw[n][k/16]) / gs_w
@@ -530,7 +530,7 @@ NVFP4_API nvfp4_status_t nvfp4_linear_w4a16(const void* x, int64_t M, int K, int
 /* ---------------------------------------------------------------------------------------------
  * moe_ffn_w4a16 — the expert FFN of a small batch with neither the activations nor the
  * intermediate quantized: route, L1 with SwiGLU, L2, weighted sum, each chosen expert's weights
- * read once (once per 8, 16 or 32 of its tokens).
+ * read once (once per 8 or 16 of its tokens).
  *
  * moe_ffn_forward's result without the two 4-bit roundings of x and h, from the same stored
  * weights, and the faster form at a decode step: nothing is padded to 128 rows.

@@ -358,24 +358,21 @@ def moe_ffn_forward_ex(x, logits, k, w1: NVFP4Weights, w2: NVFP4Weights, gs_h, d
 
 def _call_on(dev, name, *args):
     """call(name, *args, stream) with dev current, on its current stream."""
-    if dev.index == torch.cuda.current_device():
-        call(name, *args, torch._C._cuda_getCurrentRawStream(dev.index))
+    index = dev.index
+    if index == torch._C._cuda_getDevice():
+        call(name, *args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(dev):
-            call(name, *args, torch._C._cuda_getCurrentRawStream(dev.index))
+            call(name, *args, torch._C._cuda_getCurrentRawStream(index))
 
 
 def _ptrs(dev, *tensors):
     """Data pointers (None for None) of tensors that all have to be on the CUDA device dev."""
     assert dev.type == "cuda", "CUDA tensors only"
-    index, out = dev.index, []
+    index = dev.index
     for t in tensors:
-        if t is None:
-            out.append(None)
-        else:
-            assert t.get_device() == index, f"all tensors must be on {dev}"
-            out.append(t.data_ptr())
-    return out
+        assert t is None or t.get_device() == index, f"all tensors must be on {dev}"
+    return [None if t is None else t.data_ptr() for t in tensors]
 
 
 def _weight_ptrs(w: "NVFP4Weights", dev):
