@@ -511,8 +511,9 @@ NVFP4_API nvfp4_status_t moe_ffn_forward_ex(const void* x_bf16, const float* log
  *
  *   x         bf16 [M][ld] (ld >= K, ld % 8 == 0).  Every block of 16 rows goes through the weights
  *             again (out of L2 where they stay there): meant for up to a few dozen rows
- *   w, sfw    NVFP4 [N][K] (codes [N][K/2], tiled scales), gs_w device float[1]
- *   out       [M][N], out_dtype 0 = float32, 1 = bf16:
+ *   w, sfw    NVFP4 [N][K] (codes [N][K/2], tiled scales), gs_w device float[1] (positive, not
+ *             subnormal, as the quantizers make it)
+ *   out       [M][N], not overlapping x, out_dtype 0 = float32, 1 = bf16:
  *             out[m][n] = sum_k x[m][k] * E2M1(w[n][k]) * E4M3(sfw[n][k/16]) / gs_w
  *   Infinities and NaNs of x reach the outputs of their own row only.  The summation order is fixed
  *   by M, N and K (the result is reproducible).
@@ -616,7 +617,8 @@ NVFP4_API nvfp4_status_t moe_balance_loss_backward(const float* logits, int64_t 
  *   n  = r' * rstd(r') * pre_gamma       (from the unrounded r'; not made when pre_gamma is NULL)
  *   everything inside in FP32, r' and n each rounded once
  *
- *   r, r_out  [T][ld_r] and [T][H], r_dtype 0 = float32, 1 = bf16; r_out may be r (ld_r = H)
+ *   r, r_out  [T][ld_r] and [T][H], r_dtype 0 = float32, 1 = bf16; r_out may be r (ld_r = H, else
+ *             refused)
  *   y         bf16 [T][ld_y] or NULL (then no post_gamma, no gate, and r_out is not written)
  *   gate      bf16; gate_kind NVFP4_GATE_NONE (NULL: 1), _CHANNEL [H], _TOKEN [T] or _FULL [T][H]
  *   post_gamma, pre_gamma  bf16 [H] or NULL
@@ -626,7 +628,7 @@ NVFP4_API nvfp4_status_t moe_balance_loss_backward(const float* logits, int64_t 
  *   Constraints: H % 8 == 0, H <= 16384, ld_r % 8 == 0, ld_y % 8 == 0, T < 2^31; bf16 and float
  *   arrays 16-byte aligned (a token gate 2).
  *
- * Backward: the same inputs, and
+ * Backward: the same inputs (r as it was before a forward call in place), and
  *   dr_new, dn  gradients of r' [T][H] (of r's type) and of n (bf16 [T][H]); either may be NULL
  *             (zero), not both
  *   dr        [T][H] of r's type (may be dr_new); dy bf16 [T][H] (not written when y is NULL)

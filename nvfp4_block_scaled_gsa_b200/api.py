@@ -403,7 +403,7 @@ def linear_w4a16_workspace_bytes(M, N, K):
 def linear_w4a16(x, w: "NVFP4Weights", out_dtype=BF16, out=None, ws=None, status=None):
     """out (M, N) = x W^T with bf16 x (M, K) used as it is (not quantized, unlike linear()) and W
     one NVFP4 matrix (w.E == 1): for up to a few dozen rows.  out_dtype bf16 or float32; any N,
-    K % 64 == 0."""
+    K % 64 == 0; a given out must not overlap x."""
     assert x.dtype == BF16 and x.dim() == 2 and x.stride(1) == 1 and w.E == 1
     assert out_dtype in (BF16, F32)
     M, K = x.shape
@@ -467,6 +467,7 @@ def _balance_operands(logits, seq_offs, mask, dloss, dlogits):
     if seq_offs is not None:
         assert seq_offs.dtype == I32 and seq_offs.dim() == 1 and seq_offs.is_contiguous()
         S = seq_offs.numel() - 1
+    assert T < 1 << 31 and S < 1 << 31
     if mask is not None:
         assert mask.dtype in (torch.bool, U8) and mask.shape == (T,) and mask.is_contiguous()
     if dloss is not None:
@@ -575,7 +576,8 @@ def residual_norm(r, y, post_gamma=None, gate=None, scale=1.0, pre_gamma=None, e
 def residual_norm_backward(dr_new, dn, r, y, rstd_post, rstd_pre, post_gamma=None, gate=None,
                            scale=1.0, pre_gamma=None, ws=None, status=None):
     """The gradients of residual_norm from those of r' (dr_new, r's type) and n (dn, bf16), either
-    None for zero; the other arguments as given to and returned by residual_norm.  Returns a dict:
+    None for zero; the other arguments as given to (r before an update in place) and returned by
+    residual_norm.  Returns a dict:
     dr (r's type), dy (bf16), dpost_gamma and dpre_gamma (float32 (H,)), dgate (in the gate's
     shape: float32 per channel or token, bf16 (T, H)); None where there is no such input."""
     T, H, kind = _norm_operands(r, y, post_gamma, gate, pre_gamma)

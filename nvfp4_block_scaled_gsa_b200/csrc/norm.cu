@@ -674,6 +674,7 @@ extern "C" nvfp4_status_t nvfp4_residual_norm(const void* r, int r_dtype, int64_
   if (st != NVFP4_OK) return st;
   if (T == 0) return NVFP4_OK;
   if (!r || (y && !r_out) || (pre_gamma && !n_out)) return NVFP4_ERR_INVALID_ARG;
+  if (y && r_out == r && ld_r != H && T > 1) return NVFP4_ERR_INVALID_ARG;  // rows over others' input
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (r_dtype == 0) launch_forward<true>(a, s);
   else launch_forward<false>(a, s);

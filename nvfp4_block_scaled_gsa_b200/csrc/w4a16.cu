@@ -1275,6 +1275,10 @@ extern "C" nvfp4_status_t nvfp4_linear_w4a16(const void* x, int64_t M, int K, in
       (reinterpret_cast<uintptr_t>(gs_w) & 3u) || (reinterpret_cast<uintptr_t>(dev_status) & 3u))
     return NVFP4_ERR_MISALIGNED;
   if (M == 0) return NVFP4_OK;
+  // CTAs that have finished write rows of out while others still read x
+  const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), o0 = reinterpret_cast<uintptr_t>(out);
+  const uintptr_t x1 = x0 + ((M - 1) * ld + K) * 2, o1 = o0 + M * N * (out_dtype == 0 ? 4 : 2);
+  if (x0 < o1 && o0 < x1) return NVFP4_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(ws);
   int32_t* exps = reinterpret_cast<int32_t*>(base + P.exps);

@@ -231,3 +231,19 @@ def test_wrappers_refuse_tensors_off_the_gpu():
         nv.residual_norm(x, x)
     with pytest.raises(AssertionError):
         nv.residual_norm(x.half(), x)              # a type it does not take
+
+
+@pytest.mark.parametrize("x,out", [
+    (1 << 20, 1 << 20),                                  # in place
+    (1 << 20, (1 << 20) + (15 * 256 + 128) * 2 - 16),    # from x's last 16 bytes on
+    ((1 << 20) + 16 * 256 * 4 - 16, 1 << 20),            # x from out's last 16 bytes on
+])
+def test_linear_w4a16_refuses_an_output_over_its_input(L, x, out):
+    a = dict(x=ctypes.c_void_p(x), M=16, K=128, ld=256, w=F, sf=F, gs=F, N=256,
+             out=ctypes.c_void_p(out), out_dtype=0, ws=F, ws_bytes=BIG, status=None, stream=None)
+    assert L.nvfp4_linear_w4a16(*a.values()) == 1
+
+
+def test_residual_norm_refuses_dense_rows_over_strided_ones(L):
+    assert L.nvfp4_residual_norm(F, 1, 128, G, 64, 4, 64, F, None, 0, 1.0, F, 1e-6, F, F, None,
+                                 None, None) == 1
