@@ -22,9 +22,10 @@
 //
 // Both are bound by memory: 2 values of r and one each of y and n (forward), 3 of r, 2 of y and
 // one of n (backward) per element.  Forward, 8192 x 7168 with a float32 residual: 125 us, 5.6 TB/s
-// (86% of a copy's rate).  Backward, 8191 x 7168 in bf16: 144 us with the column sums, 4.9 TB/s
-// (75%); half of the issue slots are used and the rest goes to the one barrier per row, with
-// the registers (128 x 448 threads, half of them column sums) allowing one CTA per SM.
+// (86% of a copy's rate).  Backward, 8191 x 7168 with the column sums: 167 us with a float32 residual
+// (97%), 141 us with a bf16 one (76%), where the same instructions meet fewer bytes: half of the issue
+// slots are used and the rest goes to the one barrier per row, with the registers (128 x 448
+// threads, half of them column sums) allowing one CTA per SM.
 #include <atomic>
 
 #include "common.cuh"
@@ -62,7 +63,7 @@ struct Args {
   float* dpost_gamma;
   float* dpre_gamma;
   void* dgate;
-  float* part;  // [CTAs][2][H]
+  float* part;  // [clusters][2][H]
   int32_t* status;
 };
 
@@ -269,15 +270,30 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const Args A) {
 
 constexpr int kBwdChunks = 2;   // chunks of 8 columns per thread
 constexpr int kBwdStages = 3;   // rows in shared memory, at most
+constexpr int kBwdThreads = 512;
+constexpr int kBwdWidth = kBwdThreads * kBwdChunks * 8;  // columns that a CTA can take
 
-// The rows of one stage: what of dr', dn, r, y and a full gate there is, in this order.
+// How a row's columns lie on the CTAs of a cluster: `width` each, the last one fewer.  One CTA up to
+// 8192 columns, else two (4096 x 16384: 164 us, against 298 with one CTA of 1024 threads, whose 64
+// registers spilled).
+struct Columns {
+  int cluster, width, threads, per_sm;
+  explicit Columns(int H) {
+    cluster = (H + kBwdWidth - 1) / kBwdWidth;
+    width = ((H + cluster - 1) / cluster + 7) / 8 * 8;
+    threads = ((width / 8 + kBwdChunks - 1) / kBwdChunks + 31) / 32 * 32;
+    per_sm = kBwdThreads / threads;  // at 128 registers a thread
+  }
+};
+
+// A CTA's part of one row in a stage: what of dr', dn, r, y and a full gate there is, in this order.
 struct RowLayout {
   int dn, r, y, gate, bytes;
 };
 template <bool F32>
-__host__ __device__ inline RowLayout row_layout(const Args& A) {
+__host__ __device__ inline RowLayout row_layout(const Args& A, int width) {
   RowLayout L;
-  const int res = A.H * (F32 ? 4 : 2), half = A.H * 2;
+  const int res = width * (F32 ? 4 : 2), half = width * 2;
   int o = A.dr_new != nullptr ? res : 0;
   L.dn = o;
   o += A.dn != nullptr ? half : 0;
@@ -291,64 +307,110 @@ __host__ __device__ inline RowLayout row_layout(const Args& A) {
   return L;
 }
 
-// CTA b takes rows b, b + CTAs, ...  MAXT: threads at most (it sets the registers per thread);
-// FULL: the gate has a value per element (otherwise it is a factor per row or per column).  ALL: dr',
-// dn and y are all there (training's usual call), so that nothing is tested per element.
+// An array that rows are fetched from: this CTA's part of the next row, and where in a stage it goes.
+struct Source {
+  const char* next;
+  int64_t step;
+  int at, bytes;
+};
+
+// 16 bytes to shared memory of a CTA of the cluster
+__device__ __forceinline__ void st_cluster(uint32_t at, float x, float y, float z, float w) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(x), "f"(y), "f"(z), "f"(w)
+               : "memory");
+}
+
+// Cluster b (CLUSTER: of two CTAs, else one) takes rows b, b + clusters, ...  FULL: the gate has a value
+// per element (otherwise it is a factor per row or per column).  ALL: dr', dn and y are all there
+// (training's usual call), so that nothing is tested per element.
 //
 // Per element, with the row's k0 = scale * rstd(y), g_t (a token gate, or 1) and the column's
 // w = post_gamma * (a channel gate, or 1):
 //   c = k0 y w (its gradient side of the gate left out), r' = r + g_t c, u = rstd dn pre_gamma,
 //   a0 = dr' + u; sums of u r', c a0, c r'; then a = a0 - k r', dy = g_t k0 w a - k' y.
-template <bool F32, int MAXT, bool FULL, bool ALL>
-__global__ void __launch_bounds__(MAXT, 1) residual_norm_backward_kernel(const Args A, int stages) {
+template <bool F32, bool CLUSTER, bool FULL, bool ALL>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    residual_norm_backward_kernel(const Args A, int stages, int columns) {
   extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int kSources = FULL ? 5 : 4;
   __shared__ __align__(8) uint64_t bar[kBwdStages];
   __shared__ volatile int abort_flag;
+  __shared__ Source s_source[kSources];  // (each read and written by its own thread only)
   __shared__ float s_sum[2][3][32];
-  const int tid = threadIdx.x, lane = tid & 31, H = A.H;
-  const RowLayout L = row_layout<F32>(A);
-  const int res = F32 ? 4 : 2;
+  __shared__ float4 s_pair[2][2][CLUSTER ? 16 : 1];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5, H = A.H;
+  const int rank = CLUSTER ? static_cast<int>(cluster_ctarank()) : 0;
+  const int col0 = CLUSTER ? rank * columns : 0, width = CLUSTER ? min(columns, H - col0) : H;
+  const RowLayout L = row_layout<F32>(A, CLUSTER ? columns : H);
+  constexpr int res = F32 ? 4 : 2;
+  const int64_t first = CLUSTER ? blockIdx.x / 2 : blockIdx.x, step = CLUSTER ? gridDim.x / 2 : gridDim.x;
+  const bool split = CLUSTER || warps > 8;
   if (tid == 0) {
     abort_flag = 0;
-    for (int i = 0; i < stages; ++i) mbar_init(smem_u32(&bar[i]), 1);
+    for (int i = 0; i < stages; ++i) mbar_init(smem_u32(&bar[i]), split ? kSources : 1);
     fence_mbar_init();
   }
-  __syncthreads();
-  auto fetch = [&](int64_t t, int s) {  // by one thread
+  // With one CTA per SM each array is fetched by a thread of another warp: with one thread for all of
+  // them the row waited for its warp (8191 x 7168 in float32: 173 us, against 166).  With more the
+  // others cover it, and the fewer instructions count (8192 x 2048: 46.4 us, against 49.6).
+  const int source = lane * warps + warp;
+  const bool mine = split && source < kSources;
+  if (mine) {
+    const void* p = source == 0   ? A.dr_new
+                    : source == 1 ? A.dn
+                    : source == 2 ? (A.dn != nullptr ? A.r : nullptr)
+                    : source == 3 ? A.y
+                                  : (A.y != nullptr ? A.gate : nullptr);
+    const int64_t ld = source == 2 ? A.ld_r : source == 3 ? A.ld_y : H;
+    const int size = source == 0 || source == 2 ? res : 2;
+    Source& f = s_source[source];
+    f.next = static_cast<const char*>(p) + (first * ld + col0) * size;
+    f.step = step * ld * size;
+    f.at = source == 0 ? 0 : source == 1 ? L.dn : source == 2 ? L.r : source == 3 ? L.y : L.gate;
+    f.bytes = p != nullptr ? width * size : 0;
+  }
+  if (CLUSTER) cluster_sync();  // the other CTA has started
+  else __syncthreads();
+  auto fetch = [&](int64_t t, int s) {  // row t: the one behind those fetched before
     const uint32_t d = smem_u32(smem + s * L.bytes), b = smem_u32(&bar[s]);
-    mbar_arrive_expect_tx(b, L.bytes);
-    if (A.dr_new != nullptr)
-      bulk_load(d, static_cast<const char*>(A.dr_new) + t * H * res, H * res, b);
-    if (A.dn != nullptr) {
-      bulk_load(d + L.dn, A.dn + t * H, H * 2, b);
-      bulk_load(d + L.r, static_cast<const char*>(A.r) + t * A.ld_r * res, H * res, b);
-    }
-    if (A.y != nullptr) {
-      bulk_load(d + L.y, A.y + t * A.ld_y, H * 2, b);
-      if constexpr (FULL) bulk_load(d + L.gate, A.gate + t * H, H * 2, b);
+    if (mine) {
+      Source& f = s_source[source];
+      mbar_arrive_expect_tx(b, f.bytes);
+      if (f.bytes != 0) bulk_load(d + f.at, f.next, f.bytes, b);
+      f.next += f.step;
+    } else if (!split && tid == 0) {
+      mbar_arrive_expect_tx(b, L.bytes);
+      if (A.dr_new != nullptr)
+        bulk_load(d, static_cast<const char*>(A.dr_new) + t * H * res, H * res, b);
+      if (A.dn != nullptr) {
+        bulk_load(d + L.dn, A.dn + t * H, H * 2, b);
+        bulk_load(d + L.r, static_cast<const char*>(A.r) + t * A.ld_r * res, H * res, b);
+      }
+      if (A.y != nullptr) {
+        bulk_load(d + L.y, A.y + t * A.ld_y, H * 2, b);
+        if constexpr (FULL) bulk_load(d + L.gate, A.gate + t * H, H * 2, b);
+      }
     }
   };
-  const int64_t step = gridDim.x;
-  if (tid == 0)
-    for (int i = 0; i < stages; ++i)
-      if (blockIdx.x + i * step < A.T) fetch(blockIdx.x + i * step, i);
+  for (int i = 0; i < stages; ++i)
+    if (first + i * step < A.T) fetch(first + i * step, i);
 
   // this thread's columns: their factors, and their sums over the rows of a * yhat (times scale
   // and the gate, unless that is one per channel) and of dn * rhat
   F2 w[kBwdChunks][4], acc_post[kBwdChunks][4], acc_pre[kBwdChunks][4];
   uint4 wpre[kBwdChunks];
-  int cols[kBwdChunks];  // first column, or -1
+  int cols[kBwdChunks];  // first column (of the CTA's), or -1
 #pragma unroll
   for (int j = 0; j < kBwdChunks; ++j) {
-    const int c = (tid + j * blockDim.x) * 8;
-    cols[j] = c < H ? c : -1;
+    const int at = (tid + j * blockDim.x) * 8, c = col0 + at;
+    cols[j] = at < width ? at : -1;
     wpre[j] = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       w[j][i] = F2(1.0f);
       acc_post[j][i] = acc_pre[j][i] = F2(0.0f);
     }
-    if (c >= H) continue;
+    if (at >= width) continue;
     if (A.post_gamma != nullptr)
       unpack8(__ldg(reinterpret_cast<const uint4*>(A.post_gamma + c)), w[j]);
     if (A.gate_kind == GATE_CHANNEL) {
@@ -376,13 +438,13 @@ __global__ void __launch_bounds__(MAXT, 1) residual_norm_backward_kernel(const A
     }
     return v;
   };
-  Scalars next = scalars(blockIdx.x);
+  Scalars next = scalars(first);
   int it = 0, s = 0;
   uint32_t phase = 0;
   bool ok = true;
-  char* dr_row = static_cast<char*>(A.dr) + (int64_t)blockIdx.x * H * res;
-  __nv_bfloat16* dy_row = A.dy + (int64_t)blockIdx.x * H;
-  for (int64_t t = blockIdx.x; t < A.T;
+  char* dr_row = static_cast<char*>(A.dr) + (first * H + col0) * res;
+  __nv_bfloat16* dy_row = A.dy + first * H + col0;
+  for (int64_t t = first; t < A.T;
        t += step, ++it, dr_row += step * H * res, dy_row += step * H) {
     const float rs_y = next.rs_y, rs_r = next.rs_r, g_t = next.g;
     next = scalars(t + step);
@@ -434,13 +496,29 @@ __global__ void __launch_bounds__(MAXT, 1) residual_norm_backward_kernel(const A
       const float2 v = sum2[n].get();
       sums[n] = v.x + v.y;
     }
-    // the CTA's sums, in every thread; the barrier also tells that every thread has read the stage,
+    // the row's sums, in every thread; the barrier also tells that every thread has read the stage,
     // and whether all found it filled
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
       for (int n = 0; n < 3; ++n) sums[n] += __shfl_xor_sync(0xffffffffu, sums[n], o);
-    if (blockDim.x > 32) {
+    if (CLUSTER) {  // (and every warp's answer to the wait)
+      ok = __all_sync(0xffffffffu, ok) != 0;
+      if (lane < 2)
+        st_cluster(mapa_shared(smem_u32(&s_pair[it & 1][rank][warp]), lane), sums[0], sums[1], sums[2],
+                   ok ? 0.0f : 1.0f);
+      cluster_sync();
+      const float4 v = (lane & 15) < warps ? s_pair[it & 1][lane >> 4][lane & 15]
+                                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      ok = __all_sync(0xffffffffu, v.w == 0.0f) != 0;
+      sums[0] = v.x;
+      sums[1] = v.y;
+      sums[2] = v.z;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int n = 0; n < 3; ++n) sums[n] += __shfl_xor_sync(0xffffffffu, sums[n], o);
+    } else if (blockDim.x > 32) {
       if (lane == 0)
 #pragma unroll
         for (int n = 0; n < 3; ++n) s_sum[it & 1][n][tid >> 5] = sums[n];
@@ -456,11 +534,11 @@ __global__ void __launch_bounds__(MAXT, 1) residual_norm_backward_kernel(const A
       ok = __all_sync(0xffffffffu, ok) != 0;
     }
     if (!ok) break;  // all threads alike
-    if (tid == 0 && t + stages * step < A.T) fetch(t + stages * step, s);
+    if (t + stages * step < A.T) fetch(t + stages * step, s);
     // mean(u rhat) rstd per r', and sum(c a) with a = a0 - k_r r'
     const float k_r = sums[0] * inv_h * rs_r * rs_r;
     const float s_ca = sums[1] - k_r * sums[2];
-    if (tid == 0 && A.dgate != nullptr && A.gate_kind == GATE_TOKEN)
+    if (tid == 0 && rank == 0 && A.dgate != nullptr && A.gate_kind == GATE_TOKEN)
       static_cast<float*>(A.dgate)[t] = s_ca;
     // mean(d yhat) yhat rstd(y) = g_t s_ca / H * rstd(y)^2 y
     const F2 k1_2(g_t * k0), k_r2(-k_r), k_y2(post ? -g_t * s_ca * inv_h * rs_y * rs_y : 0.0f);
@@ -490,7 +568,7 @@ __global__ void __launch_bounds__(MAXT, 1) residual_norm_backward_kernel(const A
       }
       *reinterpret_cast<uint4*>(dy_row + c) = pack8(dy);
       if (FULL && A.dgate != nullptr)
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(A.dgate) + t * H + c) = pack8(dg);
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(A.dgate) + t * H + col0 + c) = pack8(dg);
     }
     if (++s == stages) {
       s = 0;
@@ -502,7 +580,7 @@ __global__ void __launch_bounds__(MAXT, 1) residual_norm_backward_kernel(const A
       report(A.status, NVFP4_DEVERR_TIMEOUT);
       volatile int never = 0;
       for (int i = 0; i < stages; ++i)
-        if (blockIdx.x + (it + i) * step < A.T)
+        if (first + (it + i) * step < A.T)
           mbar_wait_bounded(smem_u32(&bar[(it + i) % stages]), ((it + i) / stages) & 1, &never,
                             NVFP4_WAIT_TIMEOUT_NS / 4);
     }
@@ -510,7 +588,7 @@ __global__ void __launch_bounds__(MAXT, 1) residual_norm_backward_kernel(const A
   }
   pdl_trigger();
   if (A.part == nullptr) return;
-  float* part = A.part + (int64_t)blockIdx.x * 2 * H;
+  float* part = A.part + first * 2 * H + col0;
 #pragma unroll
   for (int j = 0; j < kBwdChunks; ++j) {
     if (cols[j] < 0) continue;
@@ -554,12 +632,10 @@ constexpr int kSizingSms = 148;
 
 int round32(int v) { return (v + 31) / 32 * 32; }
 
-// threads of the backward kernel, and its CTAs: as many as the SMs hold at 128 registers a thread
-int bwd_threads(int H) { return round32((H / 8 + kBwdChunks - 1) / kBwdChunks); }
-int bwd_ctas(int64_t T, int H) {
-  const int threads = bwd_threads(H);
-  const int per_sm = threads >= 512 ? 1 : 512 / threads;
-  const int64_t most = (int64_t)kSizingSms * per_sm;
+// clusters of the backward kernel: as many as the SMs hold
+int bwd_clusters(int64_t T, int H) {
+  const Columns C(H);
+  const int64_t most = (int64_t)kSizingSms * C.per_sm / C.cluster;
   return static_cast<int>(T < most ? T : most);
 }
 
@@ -599,21 +675,18 @@ void launch_forward(const Args& a, cudaStream_t s) {
   else residual_norm_kernel<F32, 1><<<grid, block, 0, s>>>(a);
 }
 
-template <bool F32, int MAXT, bool FULL, bool ALL>
-nvfp4_status_t launch_backward(const Args& a, cudaStream_t s) {
-  auto* fn = residual_norm_backward_kernel<F32, MAXT, FULL, ALL>;
-  const int threads = bwd_threads(a.H), ctas = bwd_ctas(a.T, a.H);
-  const int per_sm = threads >= 512 ? 1 : 512 / threads;
-  const int row = row_layout<F32>(a).bytes;
-  // the largest row: float32 r and dr', a full gate, kMaxH columns
-  constexpr int kMost = kMaxH * 14;
-  static_assert(kMost + 2560 <= 228 * 1024, "one row of the widest form");
+template <bool F32, bool CLUSTER, bool FULL, bool ALL>
+nvfp4_status_t launch_backward(const Args& a, const Columns& C, cudaStream_t s) {
+  auto* fn = residual_norm_backward_kernel<F32, CLUSTER, FULL, ALL>;
+  const int row = row_layout<F32>(a, C.width).bytes;
+  // the largest row: float32 r and dr', a full gate, every column that a CTA can take
+  constexpr int kMost = 2 * kBwdWidth * 14;
+  static_assert(kMost + 2560 <= 228 * 1024, "two rows of the widest form");
   // a CTA's share of an SM's 228 KB, less its static shared memory and what the system reserves
-  int room = 228 * 1024 / per_sm - 2560;
+  int room = 228 * 1024 / C.per_sm - 2560;
   room = room < kMost ? room : kMost;
-  int stages = room / (row > 0 ? row : 1);
+  int stages = room / row;
   stages = stages < 1 ? 1 : stages > kBwdStages ? kBwdStages : stages;
-  const int smem = stages * row;
   static std::atomic<uint64_t> devices_set{0};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -623,14 +696,26 @@ nvfp4_status_t launch_backward(const Args& a, cudaStream_t s) {
       return check_launch("residual_norm_backward_kernel attributes");
     devices_set.fetch_or(bit, std::memory_order_release);
   }
-  fn<<<ctas, threads, smem, s>>>(a, stages);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(bwd_clusters(a.T, a.H) * C.cluster));
+  cfg.blockDim = dim3(static_cast<unsigned>(C.threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(stages * row);
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = static_cast<unsigned>(C.cluster);
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = CLUSTER ? 1 : 0;
+  cudaLaunchKernelEx(&cfg, fn, static_cast<const Args>(a), stages, C.width);
   return check_launch("residual_norm_backward_kernel");
 }
 
 template <bool F32, bool FULL, bool ALL>
 nvfp4_status_t launch_backward(const Args& a, cudaStream_t s) {
-  return bwd_threads(a.H) <= 512 ? launch_backward<F32, 512, FULL, ALL>(a, s)
-                                 : launch_backward<F32, 1024, FULL, ALL>(a, s);
+  const Columns C(a.H);
+  return C.cluster == 1 ? launch_backward<F32, false, FULL, ALL>(a, C, s)
+                        : launch_backward<F32, true, FULL, ALL>(a, C, s);
 }
 
 template <bool F32>
@@ -683,7 +768,7 @@ extern "C" nvfp4_status_t nvfp4_residual_norm(const void* r, int r_dtype, int64_
 
 extern "C" size_t nvfp4_residual_norm_backward_workspace_size(int64_t T, int H) {
   if (T <= 0 || H <= 0 || H > kMaxH || H % 8) return 0;
-  return static_cast<size_t>((int64_t)bwd_ctas(T, H) * 2 * H * 4);
+  return static_cast<size_t>((int64_t)bwd_clusters(T, H) * 2 * H * 4);
 }
 
 extern "C" nvfp4_status_t nvfp4_residual_norm_backward(
@@ -735,7 +820,7 @@ extern "C" nvfp4_status_t nvfp4_residual_norm_backward(
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int parts = 0;
   if (T > 0) {
-    parts = bwd_ctas(T, H);
+    parts = bwd_clusters(T, H);
     st = r_dtype == 0 ? launch_backward<true>(a, s) : launch_backward<false>(a, s);
     if (st != NVFP4_OK) return st;
   }

@@ -247,3 +247,29 @@ def test_gradients_against_differences():
         mag = o[key][1].sum(0) if key == "dgate" else o[key][1]
         tol = (BWD + HALF[got[key].dtype]) * float((mag * np.abs(d)).sum()) + 1e-5
         assert abs(float((val * d).sum()) - quotient) <= tol, name
+
+
+@pytest.mark.parametrize("T,H,res,gate", [
+    (161, 8200, torch.float32, "full"),       # a row across two CTAs, several rows each, uneven halves
+    (300, 8208, torch.bfloat16, "token"),
+    (149, 16384, torch.float32, "full"),      # the widest
+    (450, 16376, torch.bfloat16, "channel"),
+    (460, 4104, torch.float32, "none"),       # one CTA per SM, the fetches shared among its warps
+])
+def test_backward_of_wide_rows(T, H, res, gate):
+    a = make(T, H, res, gate, True, True, T + H)
+    got, dr_new, dn = run_backward(a, 0.7, EPS, T)
+    check_backward(a, got, dr_new, dn, 0.7, EPS)
+    again, _, _ = run_backward(a, 0.7, EPS, T)
+    for key, v in got.items():
+        assert v is None or torch.equal(v, again[key])
+
+
+@pytest.mark.parametrize("post,pre,gate,y,with_r,with_n", [
+    (True, True, "channel", True, False, True), (True, False, "full", True, True, False),
+    (False, True, "none", False, True, True),
+])
+def test_backward_of_wide_rows_without_some_of_it(post, pre, gate, y, with_r, with_n):
+    a = make(155, 9000, torch.bfloat16, gate, post, pre, 19, y=y)
+    got, dr_new, dn = run_backward(a, 1.3, EPS, 20, with_r, with_n)
+    check_backward(a, got, dr_new, dn, 1.3, EPS)
