@@ -282,6 +282,8 @@ struct Columns {
     cluster = (H + kBwdWidth - 1) / kBwdWidth;
     width = ((H + cluster - 1) / cluster + 7) / 8 * 8;
     threads = ((width / 8 + kBwdChunks - 1) / kBwdChunks + 31) / 32 * 32;
+    // alone on its SM: as many warps for each of the four schedulers
+    if (threads > kBwdThreads / 2) threads = (threads + 127) / 128 * 128;
     per_sm = kBwdThreads / threads;  // at 128 registers a thread
   }
 };
