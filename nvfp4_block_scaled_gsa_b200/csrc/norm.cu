@@ -21,10 +21,11 @@
 // over all its rows, and a second kernel adds the CTAs' sums in order.
 //
 // Both are bound by memory: 2 values of r and one each of y and n (forward), 3 of r, 2 of y and
-// one of n (backward) per element.  Forward, 8192 x 7168 with a float32 residual: 125 us, 5.6 TB/s
-// (86% of a copy's rate).  Backward, 8191 x 7168 with the column sums: 167 us with a float32 residual
+// one of n (backward) per element.  Forward, 8192 x 7168 with a float32 residual: 120 to 125 us, 5.6
+// to 5.9 TB/s (86 to 90% of a copy's rate; CTAs that stay and copy their next rows to shared memory
+// by themselves took 178).  Backward, 8191 x 7168 with the column sums: 167 us with a float32 residual
 // (97%), 141 us with a bf16 one (76%), where the same instructions meet fewer bytes: half of the issue
-// slots are used and the rest goes to the one barrier per row, with the registers (128 x 448
+// slots are used and the rest goes to the one barrier per row, with the registers (128 x 512
 // threads, half of them column sums) allowing one CTA per SM.
 #include <atomic>
 
@@ -668,9 +669,11 @@ nvfp4_status_t check_common(const Args& a, int r_dtype) {
 template <bool F32>
 void launch_forward(const Args& a, cudaStream_t s) {
   const int n8 = a.H / 8;
-  // Enough rows for every SM several times over: 4 chunks per thread, several CTAs per SM.  Fewer:
-  // one chunk (two beyond 8192 columns), so that a row's loads are in flight at once.
-  const int chunks = a.T >= 4 * kSizingSms ? 4 : n8 <= 1024 ? 1 : 2;
+  // Enough rows for every SM several times over: 4 chunks per thread, several CTAs per SM (8192 x
+  // 7168 in bf16: 105 us, against 118 with 2 chunks), 2 up to 2048 columns (8192 x 2048: 30.2 us,
+  // against 32.7).  Fewer rows: one chunk (two beyond 8192 columns), so that a row's loads are in
+  // flight at once.
+  const int chunks = a.T >= 4 * kSizingSms ? (n8 <= 256 ? 2 : 4) : n8 <= 1024 ? 1 : 2;
   const dim3 grid(static_cast<unsigned>(a.T)), block(round32((n8 + chunks - 1) / chunks));
   if (chunks == 4) residual_norm_kernel<F32, 4><<<grid, block, 0, s>>>(a);
   else if (chunks == 2) residual_norm_kernel<F32, 2><<<grid, block, 0, s>>>(a);
