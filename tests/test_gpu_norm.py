@@ -273,3 +273,12 @@ def test_backward_of_wide_rows_without_some_of_it(post, pre, gate, y, with_r, wi
     a = make(155, 9000, torch.bfloat16, gate, post, pre, 19, y=y)
     got, dr_new, dn = run_backward(a, 1.3, EPS, 20, with_r, with_n)
     check_backward(a, got, dr_new, dn, 1.3, EPS)
+
+
+@pytest.mark.parametrize("T,H,res,gate", [(601, 2056, torch.bfloat16, "channel"),
+                                          (592, 7168, torch.float32, "full"),
+                                          (593, 16384, torch.bfloat16, "none"),
+                                          (700, 2048, torch.float32, "token")])
+def test_forward_of_many_long_rows(T, H, res, gate):
+    a = make(T, H, res, gate, True, True, T + H)
+    check_forward(a, nv.residual_norm(**a, scale=0.3, eps=EPS), 0.3, EPS)
