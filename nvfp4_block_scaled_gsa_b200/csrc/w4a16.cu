@@ -527,12 +527,15 @@ struct Ring {
                                          int bytes) const {
     bulk_load(smem_u32(stage) + kWTile + kSTile + at, x, bytes, smem_u32(&full[it % STAGES]));
   }
-  // after a wait ran out: let the copies already issued land before the CTA can exit
+  // By the copying warp behind its last copy: lets the copies already issued land before the stages
+  // are used otherwise or the CTA can exit.  Always, since a wait of the other warps may run out when
+  // this one has nothing left to wait for (otherwise they have waited for the same copies).
   __device__ __forceinline__ void drain(uint32_t issued) const {
     volatile int never = 0;
     for (uint32_t i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
-      mbar_wait_bounded(smem_u32(&full[i % STAGES]), (i / STAGES) & 1u, &never,
-                        NVFP4_WAIT_TIMEOUT_NS / 4);
+      if (!mbar_wait_bounded(smem_u32(&full[i % STAGES]), (i / STAGES) & 1u, &never,
+                             NVFP4_WAIT_TIMEOUT_NS / 4))
+        *abort_flag = 1;
   }
 };
 
@@ -609,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       copy_w(issued);
       copy_x(issued);
     }
-    if (!ok) ring.drain(issued);
+    ring.drain(issued);
   } else {
     if constexpr (XIN) {
       // pieces (token, step) warp and warp + kConsumers: lane l holds elements 8l .. 8l + 7
@@ -668,6 +671,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   // partial sums of the warps and of the cluster's CTAs -> shared memory, added in order
   __syncthreads();
   float* red = reinterpret_cast<float*>(smem);  // [KW][TOK][kRedStride]
+  const bool lost = abort_flag != 0;  // a wait ran out: NaNs, which the cluster's other CTAs pass on
   if (warp < kConsumers) {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -677,6 +681,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (t >= ntok) continue;
         float f0, f1;
         gs.factors(s_exp[t], f0, f1);
+        if (lost) f0 = __int_as_float(0x7FC00000);
 #pragma unroll
         for (int p = 0; p < me.P; ++p)
 #pragma unroll
@@ -687,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (A.splits > 1) cluster_sync();
   else __syncthreads();
   const int share = 128 / A.splits, r0 = share * split;
-  if (!abort_flag) {
+  if (!lost) {
     for (int idx = tid; idx < share * ntok; idx += kThreads) {
       const int row = r0 + idx % share, t = idx / share, n = rowblk * 128 + row;
       const float* at = red + t * kRedStride + row;
@@ -720,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
   if (A.splits > 1) cluster_sync();  // the peers have read this CTA's sums
-  if (tid == 0 && abort_flag) report(A.status, NVFP4_DEVERR_TIMEOUT);
+  if (tid == 0 && lost) report(A.status, NVFP4_DEVERR_TIMEOUT);
 }
 
 // ------------------------------------------------------------------------ streamed, in even shares
@@ -878,7 +883,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       copy_x(i, c);
       advance(c, true);
     }
-    if (!ok) ring.drain(i);
+    ring.drain(i);
   } else {
     // =========================== products ===========================
     const Lane<NT> me(warp, lane);

@@ -2,6 +2,8 @@
 refusal before anything is launched."""
 
 import ctypes
+import os
+import re
 
 import pytest
 import torch
@@ -247,3 +249,15 @@ def test_linear_w4a16_refuses_an_output_over_its_input(L, x, out):
 def test_residual_norm_refuses_dense_rows_over_strided_ones(L):
     assert L.nvfp4_residual_norm(F, 1, 128, G, 64, 4, 64, F, None, 0, 1.0, F, 1e-6, F, F, None,
                                  None, None) == 1
+
+
+def test_copying_warps_always_wait_for_their_last_copies():
+    # Another warp's wait may run out when the copying warp has nothing left to wait for, and the
+    # stages are then reused, or the CTA ends, under copies in flight.  No wait of a product can be
+    # made to run out on a GPU without a fault, so the rule is checked in the source: each of the
+    # two copying roles ends with an unconditional drain of what it issued.
+    with open(os.path.join(B.CSRC, "w4a16.cu")) as f:
+        src = f.read()
+    ends = re.findall(r"\n( *)([^\n]*ring\.drain\(\w+\);)\n  \} else \{", src)
+    assert [e[1] for e in ends] == ["ring.drain(issued);", "ring.drain(i);"]
+    assert src.count("ring.drain(") == 2
