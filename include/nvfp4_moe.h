@@ -617,8 +617,7 @@ NVFP4_API nvfp4_status_t moe_balance_loss_backward(const float* logits, int64_t 
  *   n  = r' * rstd(r') * pre_gamma       (from the unrounded r'; not made when pre_gamma is NULL)
  *   everything inside in FP32, r' and n each rounded once
  *
- *   r, r_out  [T][ld_r] and [T][H], r_dtype 0 = float32, 1 = bf16; r_out may be r (ld_r = H, else
- *             refused)
+ *   r, r_out  [T][ld_r] and [T][H], r_dtype 0 = float32, 1 = bf16
  *   y         bf16 [T][ld_y] or NULL (then no post_gamma, no gate, and r_out is not written)
  *   gate      bf16; gate_kind NVFP4_GATE_NONE (NULL: 1), _CHANNEL [H], _TOKEN [T] or _FULL [T][H]
  *   post_gamma, pre_gamma  bf16 [H] or NULL
@@ -626,12 +625,14 @@ NVFP4_API nvfp4_status_t moe_balance_loss_backward(const float* logits, int64_t 
  *   rstd_post, rstd_pre    float [T] or NULL: the rows' rstd(y) and rstd(r'), which the backward
  *             call reads
  *   Constraints: H % 8 == 0, H <= 16384, ld_r % 8 == 0, ld_y % 8 == 0, T < 2^31; bf16 and float
- *   arrays 16-byte aligned (a token gate 2).
+ *   arrays 16-byte aligned (a token gate 2).  Here and backward, an output [T][H] may be an input
+ *   [T][H] of the same type and row stride (r_out may be r with ld_r = H); outputs that overlap
+ *   inputs in another way, or one another, are refused (NVFP4_ERR_INVALID_ARG).
  *
  * Backward: the same inputs (r as it was before a forward call in place), and
  *   dr_new, dn  gradients of r' [T][H] (of r's type) and of n (bf16 [T][H]); either may be NULL
  *             (zero), not both
- *   dr        [T][H] of r's type (may be dr_new); dy bf16 [T][H] (not written when y is NULL)
+ *   dr        [T][H] of r's type; dy bf16 [T][H] (not written when y is NULL)
  *   dpost_gamma, dpre_gamma  float [H] or NULL (not wanted)
  *   dgate     float [H] (channel), float [T] (token) or bf16 [T][H] (full), or NULL
  *   ws        device scratch of nvfp4_residual_norm_backward_workspace_size(T, H) bytes (needed

@@ -548,8 +548,9 @@ def residual_norm(r, y, post_gamma=None, gate=None, scale=1.0, pre_gamma=None, e
     r (T, H) bf16 or float32, y bf16 (T, H) (rows of both may be strided) or None (r' = r: a plain
     pre-norm); gammas bf16 (H,); gate bf16, (H,) per channel, (T,) or (T, 1) per token, (T, H), or
     None (a 1-D gate is per channel where T == H).  Returns (r', n, rstd of y (T,), rstd of r'
-    (T,)): r' in r's type (out_r may be r itself), n bf16 or None without pre_gamma, the last two
-    float32 (or None) for residual_norm_backward."""
+    (T,)): r' in r's type, n bf16 or None without pre_gamma, the last two float32 (or None) for
+    residual_norm_backward.  out_r and out_n may be (T, H) inputs of the same type and row stride
+    (out_r may be r itself), and overlap nothing otherwise."""
     T, H, kind = _norm_operands(r, y, post_gamma, gate, pre_gamma)
     dev = r.device
     if y is None:

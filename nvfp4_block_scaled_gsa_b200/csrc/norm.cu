@@ -666,6 +666,44 @@ nvfp4_status_t check_common(const Args& a, int r_dtype) {
   return NVFP4_OK;
 }
 
+// An array of a call, for the check of outputs that lie over something else: [T][H] in rows of `pitch`
+// elements, or a plain vector.
+struct Span {
+  uintptr_t p, end;
+  int64_t pitch;  // 0: a vector
+  int size;       // of an element
+};
+Span rows_span(const Args& a, const void* p, int size, int64_t pitch) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  if (a.T == 1) pitch = a.H;
+  return {at, p == nullptr ? at : at + static_cast<uintptr_t>((a.T - 1) * pitch + a.H) * size, pitch, size};
+}
+Span vector_span(const void* p, int64_t n, int size) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  return {at, p == nullptr ? at : at + static_cast<uintptr_t>(n) * size, 0, size};
+}
+// Outputs apart from one another and from the inputs.  Rows may take the place of the very same rows
+// (address, pitch and type): a row is read by the threads that write it, before they do.  Rows over
+// other rows would be written by one CTA while another still reads them.
+template <int O, int I>
+bool outputs_apart(const Span (&outs)[O], const Span (&ins)[I]) {
+  auto overlap = [](const Span& x, const Span& y) { return x.p < y.end && y.p < x.end; };
+  for (int i = 0; i < O; ++i) {
+    const Span& o = outs[i];
+    for (int j = 0; j < i; ++j)
+      if (overlap(o, outs[j])) return false;
+    for (const Span& in : ins)
+      if (overlap(o, in) &&
+          !(o.p == in.p && o.pitch != 0 && o.pitch == in.pitch && o.size == in.size))
+        return false;
+  }
+  return true;
+}
+Span gate_span(const Args& a) {
+  return a.gate_kind == GATE_FULL ? rows_span(a, a.gate, 2, a.H)
+                                  : vector_span(a.gate, a.gate_kind == GATE_TOKEN ? a.T : a.H, 2);
+}
+
 template <bool F32>
 void launch_forward(const Args& a, cudaStream_t s) {
   const int n8 = a.H / 8;
@@ -764,7 +802,14 @@ extern "C" nvfp4_status_t nvfp4_residual_norm(const void* r, int r_dtype, int64_
   if (st != NVFP4_OK) return st;
   if (T == 0) return NVFP4_OK;
   if (!r || (y && !r_out) || (pre_gamma && !n_out)) return NVFP4_ERR_INVALID_ARG;
-  if (y && r_out == r && ld_r != H && T > 1) return NVFP4_ERR_INVALID_ARG;  // rows over others' input
+  const int res = r_dtype == 0 ? 4 : 2;
+  const Span outs[] = {rows_span(a, y ? r_out : nullptr, res, H),
+                       rows_span(a, pre_gamma ? n_out : nullptr, 2, H),
+                       vector_span(post_gamma ? rstd_post : nullptr, T, 4),
+                       vector_span(pre_gamma ? rstd_pre : nullptr, T, 4)};
+  const Span ins[] = {rows_span(a, r, res, ld_r), rows_span(a, y, 2, ld_y),
+                      vector_span(post_gamma, H, 2), vector_span(pre_gamma, H, 2), gate_span(a)};
+  if (!outputs_apart(outs, ins)) return NVFP4_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (r_dtype == 0) launch_forward<true>(a, s);
   else launch_forward<false>(a, s);
@@ -821,6 +866,21 @@ extern "C" nvfp4_status_t nvfp4_residual_norm_backward(
   else if (T > 0 &&
            (ws == nullptr || ws_bytes < nvfp4_residual_norm_backward_workspace_size(T, H)))
     return NVFP4_ERR_WORKSPACE_TOO_SMALL;
+  if (T > 0) {
+    const int res = r_dtype == 0 ? 4 : 2;
+    const Span outs[] = {
+        rows_span(a, dr, res, H), rows_span(a, y ? dy : nullptr, 2, H), vector_span(dpost_gamma, H, 4),
+        vector_span(dpre_gamma, H, 4),
+        gate_kind == GATE_FULL ? rows_span(a, dgate, 2, H)
+                               : vector_span(dgate, gate_kind == GATE_TOKEN ? T : H, 4),
+        vector_span(a.part, columns ? (int64_t)bwd_clusters(T, H) * 2 * H : 0, 4)};
+    const Span ins[] = {rows_span(a, dr_new, res, H), rows_span(a, dn, 2, H),
+                        rows_span(a, dn ? r : nullptr, res, ld_r), rows_span(a, y, 2, ld_y),
+                        vector_span(post_gamma, H, 2), vector_span(pre_gamma, H, 2), gate_span(a),
+                        vector_span(post_gamma ? rstd_post : nullptr, T, 4),
+                        vector_span(dn ? rstd_pre : nullptr, T, 4)};
+    if (!outputs_apart(outs, ins)) return NVFP4_ERR_INVALID_ARG;
+  }
   a.status = dev_status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int parts = 0;

@@ -261,3 +261,65 @@ def test_copying_warps_always_wait_for_their_last_copies():
     ends = re.findall(r"\n( *)([^\n]*ring\.drain\(\w+\);)\n  \} else \{", src)
     assert [e[1] for e in ends] == ["ring.drain(issued);", "ring.drain(i);"]
     assert src.count("ring.drain(") == 2
+
+
+def at(base, off):
+    return ctypes.c_void_p(base + off)
+
+
+ROW = 64 * 2  # bytes of a bf16 row of 64
+
+
+# T = 4 rows of 64, r float32 or bf16 with rows of ld_r, y bf16 with rows of ld_y; the base addresses
+# are far apart unless said otherwise
+@pytest.mark.parametrize("change,code", [
+    (dict(r_out=at(1 << 20, ROW)), 1),                      # one row behind r
+    (dict(r_out=at(1 << 20, -ROW)), 1),                     # one row in front of it
+    (dict(r_out=at(1 << 20, 4 * ROW - 16)), 1),             # over r's last 16 bytes
+    (dict(n_out=at(1 << 20, ROW)), 1),
+    (dict(n_out=at(1 << 21, 2 * ROW)), 1),                  # over y
+    (dict(ld_r=128, n_out=at(1 << 20, 0)), 1),              # dense rows over strided ones
+    (dict(ld_y=128, n_out=at(1 << 21, 0)), 1),
+    (dict(ld_y=128, r_out=at(1 << 21, 0)), 1),
+    (dict(dtype=0, n_out=at(1 << 20, 0)), 1),               # bf16 rows over float32 ones
+    (dict(n_out=at(1 << 22, 3 * ROW)), 1),                  # over r_out
+    (dict(post=at(1 << 22, 0)), 1),                         # r_out over a gamma
+    (dict(pre=at(1 << 23, 2 * ROW)), 1),
+    (dict(gate=at(1 << 22, 128), kind=3), 1),               # r_out over part of a full gate
+    (dict(gate=at(1 << 23, 4 * ROW - 16), kind=1), 1),
+    (dict(rs1=at(1 << 20, 0)), 1),                          # the rows' rstd over r
+    (dict(rs2=at(1 << 22, 0)), 1),                          # ... over r_out
+])
+def test_residual_norm_refuses_outputs_over_other_rows(L, change, code):
+    a = dict(r=at(1 << 20, 0), dtype=1, ld_r=64, y=at(1 << 21, 0), ld_y=64, T=4, H=64,
+             post=at(1 << 24, 0), gate=None, kind=0, scale=1.0, pre=at(1 << 25, 0), eps=1e-6,
+             r_out=at(1 << 22, 0), n_out=at(1 << 23, 0), rs1=at(1 << 26, 0), rs2=at(1 << 27, 0),
+             stream=None)
+    a.update(change)
+    assert L.nvfp4_residual_norm(*a.values()) == code
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(dr=at(1 << 20, ROW)), 1),                         # one row behind dr_new
+    (dict(dr=at(1 << 22, -ROW)), 1),                        # one row in front of r
+    (dict(dy=at(1 << 21, 2 * ROW)), 1),                     # over other rows of dn
+    (dict(dy=at(1 << 23, ROW)), 1),                         # ... of y
+    (dict(ld_y=128, dy=at(1 << 23, 0)), 1),                 # dense rows over strided ones
+    (dict(ld_r=128, dr=at(1 << 22, 0)), 1),
+    (dict(dtype=0, dr=at(1 << 21, 0)), 1),                  # float32 rows over bf16 ones
+    (dict(dy=at(1 << 24, ROW)), 1),                         # over dr
+    (dict(gate=at(1 << 27, 0), kind=3, dgate=at(1 << 27, ROW)), 1),
+    (dict(gate=at(1 << 24, 0), kind=2), 1),                 # dr over a gate per token
+    (dict(dpost=at(1 << 20, 0)), 1),
+    (dict(dpre=at(1 << 28, 128)), 1),                       # over dpost
+    (dict(ws=at(1 << 24, 0)), 1),                           # the workspace over dr
+    (dict(rs2=at(1 << 25, 0)), 1),                          # dy over the rows' rstd
+])
+def test_residual_norm_backward_refuses_outputs_over_other_rows(L, change, code):
+    a = dict(dr_new=at(1 << 20, 0), dn=at(1 << 21, 0), r=at(1 << 22, 0), dtype=1, ld_r=64,
+             y=at(1 << 23, 0), ld_y=64, T=4, H=64, post=at(1 << 26, 0), gate=None, kind=0, scale=1.0,
+             pre=at((1 << 26) + 4096, 0), rs1=at(1 << 29, 0), rs2=at((1 << 29) + 64, 0),
+             dr=at(1 << 24, 0), dy=at(1 << 25, 0), dpost=at(1 << 28, 0), dpre=at((1 << 28) + 256, 0),
+             dgate=None, ws=at(1 << 30, 0), ws_bytes=1 << 16, status=None, stream=None)
+    a.update(change)
+    assert L.nvfp4_residual_norm_backward(*a.values()) == code

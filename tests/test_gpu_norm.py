@@ -282,3 +282,56 @@ def test_backward_of_wide_rows_without_some_of_it(post, pre, gate, y, with_r, wi
 def test_forward_of_many_long_rows(T, H, res, gate):
     a = make(T, H, res, gate, True, True, T + H)
     check_forward(a, nv.residual_norm(**a, scale=0.3, eps=EPS), 0.3, EPS)
+
+
+@pytest.mark.parametrize("T,H", [(1, 64), (5, 2056), (700, 520)])
+@pytest.mark.parametrize("res", [torch.bfloat16, torch.float32])
+def test_outputs_in_the_place_of_the_same_rows(T, H, res):
+    a = make(T, H, res, "full", True, True, T + H)
+    want = nv.residual_norm(**a, eps=EPS)
+    same = res == torch.bfloat16
+    for place_r, place_n in [("r", "y"), ("r", "gate")] + ([("y", "r"), ("gate", "y")] if same else []):
+        b = {k: v.clone() for k, v in a.items()}
+        got = nv.residual_norm(**b, eps=EPS, out_r=b[place_r], out_n=b[place_n])
+        assert got[0].data_ptr() == b[place_r].data_ptr()
+        for g, w in zip(got, want):
+            assert torch.equal(g, w)
+
+
+def test_outputs_over_other_rows_are_refused():
+    a = make(4, 64, torch.bfloat16, "none", True, True, 3)
+    buf = torch.zeros(9, 64, dtype=torch.bfloat16, device=DEV)
+    buf[:4] = a["r"]
+    a["r"] = buf[:4]
+    for kw in (dict(out_r=buf[1:5]), dict(out_n=buf[3:7]), dict(out_r=buf[4:8], out_n=buf[5:9])):
+        with pytest.raises(nv.Nvfp4Error):
+            nv.residual_norm(**a, **kw)
+    wide = torch.zeros(4, 128, dtype=torch.bfloat16, device=DEV)
+    a["r"] = wide[:, :64]
+    with pytest.raises(nv.Nvfp4Error):
+        nv.residual_norm(**a, out_n=wide.view(8, 64)[:4])
+    out = nv.residual_norm(**a, out_n=buf[:4], out_r=buf[4:8])  # apart
+    assert out[1].data_ptr() == buf.data_ptr()
+
+
+def test_backward_in_place_of_its_gradients():
+    """The C call with dr over dr', dy over dn (bf16 residual) or y."""
+    for res, over in ((torch.bfloat16, "dn"), (torch.float32, "y")):
+        a = make(300, 520, res, "channel", True, True, 4)
+        want, dr_new, dn = run_backward(a, 0.9, EPS, 5)
+        _, _, rs_y, rs_r = nv.residual_norm(**a, scale=0.9, eps=EPS)
+        T, H = a["r"].shape
+        dr, dy = dr_new.clone(), {"dn": dn, "y": a["y"]}[over].clone()
+        dn_, y_ = (dy, a["y"]) if over == "dn" else (dn, dy)
+        grads = [torch.empty(H, device=DEV) for _ in range(3)]
+        ws = torch.empty(int(nv.lib().nvfp4_residual_norm_backward_workspace_size(T, H)),
+                         dtype=torch.uint8, device=DEV)
+        p = torch.Tensor.data_ptr
+        rc = nv.lib().nvfp4_residual_norm_backward(
+            p(dr), p(dn_), p(a["r"]), 0 if res == torch.float32 else 1, H, p(y_), H, T, H,
+            p(a["post_gamma"]), p(a["gate"]), 1, 0.9, p(a["pre_gamma"]), p(rs_y), p(rs_r), p(dr),
+            p(dy), p(grads[0]), p(grads[1]), p(grads[2]), p(ws), ws.numel(), None,
+            torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        for g, key in zip([dr, dy] + grads, ("dr", "dy", "dpost_gamma", "dpre_gamma", "dgate")):
+            assert torch.equal(g, want[key]), key
