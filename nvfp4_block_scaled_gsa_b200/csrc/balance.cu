@@ -138,6 +138,12 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// a / b from y = 1 / b, which may be a few steps off: the remainder of a y is exact in one fma, and adding
+// its share leaves about half a step.  a = b gives 1 to the bit.
+__device__ __forceinline__ float quotient(float a, float b, float y) {
+  const float q = a * y;
+  return fmaf(fmaf(-q, b, a), y, q);
+}
 
 // L lanes per token, 4 * NV logits each; a warp takes 32 / L consecutive tokens at a time.  Many
 // logits per lane keep the shuffles of the row sums few (40961 x 160 at 32 lanes of 8 was bound by
@@ -231,8 +237,8 @@ __global__ void __launch_bounds__(kThreads, 3) balance_kernel(const Args A) {
     const int n = s == s_cta ? n_cta : ld_after(A.tokens + s);
     inside = n > 0;
     per_token = inside ? A.alpha / static_cast<float>(n) * share : 0.0f;
-    const float unit =
-        inside ? static_cast<float>(E) / (static_cast<float>(A.k) * static_cast<float>(n)) : 0.0f;
+    const float even = inside ? static_cast<float>(A.k) * static_cast<float>(n) : 1.0f;
+    const float per_even = inside ? 1.0f / even : 0.0f;
     int c[kSlots];
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) {
@@ -241,7 +247,8 @@ __global__ void __launch_bounds__(kThreads, 3) balance_kernel(const Args A) {
         c[i] = s == s_cta ? s_counts[expert(i)] : ld_after(A.counts + (int64_t)s * E + expert(i));
     }
 #pragma unroll
-    for (int i = 0; i < kSlots; ++i) f[i] = static_cast<float>(c[i]) * unit;
+    for (int i = 0; i < kSlots; ++i)
+      f[i] = quotient(static_cast<float>(c[i]) * static_cast<float>(E), even, per_even);
   };
 
   double sum = 0.0;
@@ -275,8 +282,9 @@ __global__ void __launch_bounds__(kThreads, 3) balance_kernel(const Args A) {
       z += __shfl_xor_sync(0xffffffffu, z, o);
       dot += __shfl_xor_sync(0xffffffffu, dot, o);
     }
-    const float inv = z == 0.0f ? 0.0f : rcp_approx(z);
-    const float vt = dot * inv;
+    // Where every f is 1 (an even load), dot is z to the bit, so vt is 1 and the gradient exactly 0.
+    const float y = z == 0.0f ? 0.0f : rcp_approx(z);
+    const float inv = quotient(1.0f, z, y), vt = quotient(dot, z, y);
     if (A.loss != nullptr && counted && l == 0)
       sum += static_cast<double>(coef) * static_cast<double>(vt);
     if (A.dlogits != nullptr && t < A.T) {

@@ -195,3 +195,19 @@ def test_counts_of_the_routers_own_output():
     # the row map's segments hold exactly these counts, padded to 128
     seg = (r["offs"][1:] - r["offs"][:-1]).long()
     assert torch.equal(seg, (counts[0].long() + 127) // 128 * 128) and tokens.item() == T
+
+
+@pytest.mark.parametrize("T,E", [(5, 3), (49, 2), (100, 5), (333, 8), (41, 32), (640, 6)])
+def test_a_load_that_is_even_by_itself_has_no_gradient(T, E):
+    # every token names every expert: f is 1 and f - v exactly 0, whatever the probabilities
+    rng = np.random.default_rng(T)
+    z = (rng.normal(size=(T, E)) * 3).astype(np.float32)
+    ids = np.stack([rng.permutation(E) for _ in range(T)]).astype(np.int32)
+    dloss = torch.full((1,), 3.0, device=DEV)
+    for keep in (None, rng.random(T) > 0.2):
+        at = dict(mask=None if keep is None else to_dev(keep))
+        loss, counts, tokens, d = nv.balance_loss(to_dev(z), to_dev(ids), 0.25, want_grad=True,
+                                                  dloss=dloss, **at)
+        assert abs(loss.item() - 0.25) <= REL * 0.25
+        assert (d == 0).all()
+        assert (nv.balance_loss_backward(to_dev(z), counts, tokens, E, 0.25, dloss=dloss, **at) == 0).all()
