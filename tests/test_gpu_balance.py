@@ -211,3 +211,18 @@ def test_a_load_that_is_even_by_itself_has_no_gradient(T, E):
         assert abs(loss.item() - 0.25) <= REL * 0.25
         assert (d == 0).all()
         assert (nv.balance_loss_backward(to_dev(z), counts, tokens, E, 0.25, dloss=dloss, **at) == 0).all()
+
+
+def test_far_probabilities_keep_their_bits():
+    # Expert 0 takes every slot and, up to e^-30, all of the probability: z = 1, v = E, and the
+    # gradient elsewhere is -a E p.  The logits' differences, a and E are exact, so what is left of
+    # the relative error is the exponential's 2 * 2^-24 and six roundings: 2^-21.
+    T, E = 64, 32
+    z = -np.random.default_rng(11).integers(30 * 8, 80 * 8, size=(T, E)).astype(np.float32) / 8
+    z[:, 0] = 0.0
+    ids = np.zeros((T, 1), np.int32)
+    ref = P.balance(z, ids, 0.5)[3]
+    for shift in (0.0, 17.25):  # of the whole row: the same differences
+        d = nv.balance_loss(to_dev(z + np.float32(shift)), to_dev(ids), 0.5, want_grad=True)[3]
+        err = np.abs(d.double().cpu().numpy() - ref)[:, 1:] / np.abs(ref[:, 1:])
+        assert err.max() <= 2.0 ** -21, err.max()
