@@ -1016,7 +1016,8 @@ __global__ void __launch_bounds__(512) swiglu_kernel(const float* part, const Sp
         sum_planes<2>(base, {row, row + 16}, n_pad,
                       block_planes(S, per, unit * S.blocks + row / 128), v);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = v[0][i] * v[1][i] / (1.0f + expf(-v[0][i]));
+        for (int i = 0; i < 4; ++i)  // silu first: gate * up alone may not be finite
+          h[i] = v[0][i] / (1.0f + expf(-v[0][i])) * v[1][i];
       },
       I, hf + s * steps * kStepX, kStepX, exps + s, red);
 }

@@ -306,3 +306,21 @@ def test_ffn_on_another_stream_and_in_a_graph():
         torch.cuda.synchronize()
         assert torch.equal(out, want[i])
         assert torch.equal(out2, nv.moe_ffn_w4a16(want[i], lgs[i], k, w1, w2))
+
+
+@pytest.mark.parametrize("big", [1e4, 1e30])
+def test_ffn_of_gates_far_below_zero(big):
+    # g = -x0 and u = x0 for every feature: silu(-big) * big is 0 although big * big may not be finite
+    H, I = 128, 64
+    w1, w2 = np.zeros((1, 2 * I, H), np.float32), np.ones((1, H, I), np.float32)
+    w1[:, :I, 0], w1[:, I:, 0] = -1.0, 1.0
+    q1, q2 = M.QuantWeights.from_float(w1), M.QuantWeights.from_float(w2)
+    f1, f2 = q1.dequant(0)[None], q2.dequant(0)[None]
+    x = bf16(np.zeros((3, H)))
+    x[:, 0] = torch.tensor([big, -1.0, 2.0])
+    ids, wts = np.zeros((3, 1), np.int32), np.ones((3, 1), np.float32)
+    got = nv.moe_ffn_w4a16(x.to(DEV), None, 1, upload_weights(q1, w1=True), upload_weights(q2),
+                           ids=to_dev(ids), weights=to_dev(wts))
+    assert (got[0] == 0).all()
+    with np.errstate(over="ignore"):
+        check_ffn(got, x, ids, wts, f1, f2)
