@@ -418,6 +418,13 @@ nvfp4_status_t check_shape(int T, int E, int k, int64_t ld, int S, const int32_t
   return NVFP4_OK;
 }
 
+// Whether the gradient's rows lie over any of the logits, which other warps may still have to read.
+bool over_logits(const float* logits, int64_t ld, int T, int E, const float* dlogits) {
+  if (dlogits == nullptr || T == 0) return false;
+  const uintptr_t l = reinterpret_cast<uintptr_t>(logits), d = reinterpret_cast<uintptr_t>(dlogits);
+  return d < l + ((int64_t)(T - 1) * ld + E) * 4 && l < d + (int64_t)T * E * 4;
+}
+
 }  // namespace
 }  // namespace nvfp4
 
@@ -440,12 +447,13 @@ extern "C" nvfp4_status_t moe_balance_loss(const float* logits, int64_t ld, int 
   nvfp4_status_t st = check_shape(T, E, k, ld, S, seq_offs);
   if (st != NVFP4_OK) return st;
   if (!counts || !tokens || !loss || !ws) return NVFP4_ERR_INVALID_ARG;
-  if (T > 0 && (!logits || !topk_ids || logits == dlogits)) return NVFP4_ERR_INVALID_ARG;
+  if (T > 0 && (!logits || !topk_ids)) return NVFP4_ERR_INVALID_ARG;
   if (ws_bytes < moe_balance_loss_workspace_size(T, E)) return NVFP4_ERR_WORKSPACE_TOO_SMALL;
   const void* ptrs4[] = {logits, topk_ids, seq_offs, counts, tokens, loss, dloss, dlogits, dev_status};
   for (const void* p : ptrs4)
     if (reinterpret_cast<uintptr_t>(p) & 3u) return NVFP4_ERR_MISALIGNED;
   if (!aligned16(ws)) return NVFP4_ERR_MISALIGNED;
+  if (over_logits(logits, ld, T, E, dlogits)) return NVFP4_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(ws);
   uint32_t* ticket = reinterpret_cast<uint32_t*>(base);
@@ -494,10 +502,11 @@ extern "C" nvfp4_status_t moe_balance_loss_backward(const float* logits, int64_t
   const nvfp4_status_t st = check_shape(T, E, k, ld, S, seq_offs);
   if (st != NVFP4_OK) return st;
   if (!counts || !tokens) return NVFP4_ERR_INVALID_ARG;
-  if (T > 0 && (!logits || !dlogits || logits == dlogits)) return NVFP4_ERR_INVALID_ARG;
+  if (T > 0 && (!logits || !dlogits)) return NVFP4_ERR_INVALID_ARG;
   const void* ptrs4[] = {logits, seq_offs, counts, tokens, dloss, dlogits};
   for (const void* p : ptrs4)
     if (reinterpret_cast<uintptr_t>(p) & 3u) return NVFP4_ERR_MISALIGNED;
+  if (over_logits(logits, ld, T, E, dlogits)) return NVFP4_ERR_INVALID_ARG;
   if (T == 0) return NVFP4_OK;
   Args a{};
   a.logits = logits;

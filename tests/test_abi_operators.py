@@ -323,3 +323,23 @@ def test_residual_norm_backward_refuses_outputs_over_other_rows(L, change, code)
              dgate=None, ws=at(1 << 30, 0), ws_bytes=1 << 16, status=None, stream=None)
     a.update(change)
     assert L.nvfp4_residual_norm_backward(*a.values()) == code
+
+
+# T = 16 rows of 8 logits, in rows of ld
+@pytest.mark.parametrize("change", [
+    dict(dlogits=at(1 << 20, 32)),                     # one row behind the logits
+    dict(dlogits=at(1 << 20, -32)),
+    dict(dlogits=at(1 << 20, 15 * 32 + 28)),           # over their last word
+    dict(ld=16, dlogits=at(1 << 20, 15 * 64 + 28)),    # the same in strided rows
+    dict(ld=16, dlogits=at(1 << 20, 32)),              # dense rows among strided ones
+])
+def test_balance_loss_refuses_a_gradient_over_the_logits(L, change):
+    a = dict(logits=at(1 << 20, 0), ld=8, T=16, E=8, k=2, ids=F, offs=None, S=1, mask=None, alpha=0.01,
+             counts=G, tokens=G, loss=G, dloss=None, dlogits=None, acc=0, ws=G, ws_bytes=BIG,
+             status=None, stream=None)
+    a.update(change)
+    assert L.moe_balance_loss(*a.values()) == 1
+    b = dict(logits=at(1 << 20, 0), ld=8, T=16, E=8, k=2, counts=G, tokens=G, offs=None, S=1,
+             mask=None, alpha=0.01, dloss=None, dlogits=None, acc=1, stream=None)
+    b.update(change)
+    assert L.moe_balance_loss_backward(*b.values()) == 1
