@@ -546,7 +546,8 @@ NVFP4_API nvfp4_status_t nvfp4_linear_w4a16(const void* x, int64_t M, int K, int
  *   topk_w    float [T][k], not read for dropped slots
  *   w1, sfw1, gs_w1  NVFP4 [E*2I][H] in the gate/up interleave of moe_w1_row_map, float[E]
  *   w2, sfw2, gs_w2  NVFP4 [E*H][I], float[E]
- *   out_bf16  bf16 [T][H]; a token whose slots are all dropped gets zeros
+ *   out_bf16  bf16 [T][H], not overlapping topk_w (it may be x); a token whose slots are all dropped
+ *             gets zeros
  *   ws        device scratch of moe_ffn_w4a16_workspace_size() bytes, 256-byte aligned
  *   Constraints: H % 128 == 0, I % 64 == 0, 1 <= k <= E <= 256, k <= 32,
  *   T*k <= NVFP4_W4A16_MAX_SLOTS (larger batches: moe_ffn_forward).

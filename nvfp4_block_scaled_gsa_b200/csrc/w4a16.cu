@@ -1347,6 +1347,11 @@ extern "C" nvfp4_status_t moe_ffn_w4a16(const void* x_bf16, const float* logits,
   for (const void* p : ptrs4)
     if (reinterpret_cast<uintptr_t>(p) & 3u) return NVFP4_ERR_MISALIGNED;
   if (reinterpret_cast<uintptr_t>(ws) & 255u) return NVFP4_ERR_MISALIGNED;
+  // CTAs that have finished write rows of out while others still read the weights (x and the ids are
+  // read by the first kernel alone: out may be x)
+  const uintptr_t o0 = reinterpret_cast<uintptr_t>(out_bf16), w0 = reinterpret_cast<uintptr_t>(topk_w);
+  if (topk_w != nullptr && o0 < w0 + (int64_t)T * k * 4 && w0 < o0 + (int64_t)T * H * 2)
+    return NVFP4_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(ws);
   auto i32 = [&](int64_t off) { return reinterpret_cast<int32_t*>(base + off); };

@@ -343,3 +343,14 @@ def test_balance_loss_refuses_a_gradient_over_the_logits(L, change):
              mask=None, alpha=0.01, dloss=None, dlogits=None, acc=1, stream=None)
     b.update(change)
     assert L.moe_balance_loss_backward(*b.values()) == 1
+
+
+@pytest.mark.parametrize("out,w", [
+    (1 << 20, (1 << 20) + 4 * 256 * 2 - 4),   # the routing weights in out's last bytes
+    ((1 << 20) + 16, 1 << 20),                # out from inside the routing weights on
+])
+def test_moe_ffn_w4a16_refuses_an_output_over_its_routing_weights(L, out, w):
+    a = dict(x=G, logits=None, ids=G, w=ctypes.c_void_p(w), T=4, H=256, I=128, E=8, k=2, w1=G, sf1=G,
+             gs1=G, w2=G, sf2=G, gs2=G, out=ctypes.c_void_p(out), ws=G, ws_bytes=BIG, status=None,
+             stream=None)
+    assert L.moe_ffn_w4a16(*a.values()) == 1

@@ -324,3 +324,12 @@ def test_ffn_of_gates_far_below_zero(big):
     assert (got[0] == 0).all()
     with np.errstate(over="ignore"):
         check_ffn(got, x, ids, wts, f1, f2)
+
+
+def test_ffn_output_in_the_place_of_its_input():
+    T, H, I, E, k = 9, 256, 128, 6, 2
+    w1, w2, _, _ = make_experts(E, H, I, seed=14)
+    x = bf16(np.random.default_rng(14).normal(size=(T, H))).to(DEV)
+    lg = to_dev(np.random.default_rng(15).normal(size=(T, E)).astype(np.float32))
+    want = nv.moe_ffn_w4a16(x, lg, k, w1, w2)
+    assert torch.equal(nv.moe_ffn_w4a16(x, lg, k, w1, w2, out=x), want)
