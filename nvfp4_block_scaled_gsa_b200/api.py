@@ -487,6 +487,7 @@ def balance_loss(logits, ids, alpha, seq_offs=None, mask=None, want_grad=False, 
     padding tokens.  Returns (loss (1,), counts int32 (S, E), tokens int32 (S,), dlogits or
     None).  want_grad: dlogits (T, E) float32, times dloss (device float[1], default 1), in the
     same pass; a given dlogits is added to."""
+    assert dlogits is None or want_grad, "dlogits is for want_grad=True"
     accumulate = dlogits is not None
     T, E, S = _balance_operands(logits, seq_offs, mask, dloss, dlogits)
     dev = logits.device

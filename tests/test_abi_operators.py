@@ -354,3 +354,9 @@ def test_moe_ffn_w4a16_refuses_an_output_over_its_routing_weights(L, out, w):
              gs1=G, w2=G, sf2=G, gs2=G, out=ctypes.c_void_p(out), ws=G, ws_bytes=BIG, status=None,
              stream=None)
     assert L.moe_ffn_w4a16(*a.values()) == 1
+
+
+def test_balance_loss_takes_a_gradient_buffer_only_when_it_is_wanted():
+    with pytest.raises(AssertionError, match="want_grad"):
+        nv.balance_loss(torch.zeros(2, 4), torch.zeros(2, 1, dtype=torch.int32), 0.1,
+                        dlogits=torch.zeros(2, 4))
