@@ -553,6 +553,7 @@ def residual_norm(r, y, post_gamma=None, gate=None, scale=1.0, pre_gamma=None, e
     residual_norm_backward.  out_r and out_n may be (T, H) inputs of the same type and row stride
     (out_r may be r itself), and overlap nothing otherwise."""
     T, H, kind = _norm_operands(r, y, post_gamma, gate, pre_gamma)
+    assert out_n is None or pre_gamma is not None, "out_n needs a pre_gamma"
     dev = r.device
     if y is None:
         assert out_r is None

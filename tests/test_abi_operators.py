@@ -360,3 +360,9 @@ def test_balance_loss_takes_a_gradient_buffer_only_when_it_is_wanted():
     with pytest.raises(AssertionError, match="want_grad"):
         nv.balance_loss(torch.zeros(2, 4), torch.zeros(2, 1, dtype=torch.int32), 0.1,
                         dlogits=torch.zeros(2, 4))
+
+
+def test_residual_norm_takes_no_output_that_it_would_not_fill():
+    x = torch.zeros(2, 64, dtype=torch.bfloat16)
+    with pytest.raises(AssertionError, match="pre_gamma"):
+        nv.residual_norm(x, x, out_n=torch.zeros_like(x))
