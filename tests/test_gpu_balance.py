@@ -226,3 +226,21 @@ def test_far_probabilities_keep_their_bits():
         d = nv.balance_loss(to_dev(z + np.float32(shift)), to_dev(ids), 0.5, want_grad=True)[3]
         err = np.abs(d.double().cpu().numpy() - ref)[:, 1:] / np.abs(ref[:, 1:])
         assert err.max() <= 2.0 ** -21, err.max()
+
+
+@pytest.mark.parametrize("T,E,k,S,mask,edge", [
+    (8193, 256, 8, 1, False, False), (8193, 256, 8, 700, True, True), (20001, 160, 6, 13, True, True),
+    (9001, 255, 4, 5, True, False), (120001, 2, 1, 3, True, True), (70011, 6, 3, 2000, False, True),
+])
+def test_long_batches(T, E, k, S, mask, edge):
+    """More token groups than warps: a warp takes several, and meets sequences that its CTA did not
+    start in; more CTAs than one round of the last sum."""
+    assert int(nv.lib().moe_balance_loss_workspace_size(T, E)) > 256 + 256 * 8
+    z, ids, offs, keep = problem(T, E, k, T + E, S, mask, edge)
+    at = dict(seq_offs=to_dev(offs), mask=None if keep is None else to_dev(keep))
+    dloss = torch.full((1,), 1.75, device=DEV)
+    loss, counts, tokens, d = nv.balance_loss(to_dev(z), to_dev(ids), 0.3, want_grad=True, dloss=dloss,
+                                              **at)
+    check(z, ids, 0.3, offs, keep, 1.75, loss, counts, tokens, d)
+    assert torch.equal(nv.balance_loss_backward(to_dev(z), counts, tokens, k, 0.3, dloss=dloss, **at), d)
+    assert torch.equal(nv.balance_loss(to_dev(z), to_dev(ids), 0.3, **at)[0], loss)

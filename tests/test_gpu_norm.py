@@ -335,3 +335,20 @@ def test_backward_in_place_of_its_gradients():
         assert rc == 0
         for g, key in zip([dr, dy] + grads, ("dr", "dy", "dpost_gamma", "dpre_gamma", "dgate")):
             assert torch.equal(g, want[key]), key
+
+
+@pytest.mark.parametrize("gate", ["none", "channel", "token", "full"])
+@pytest.mark.parametrize("T,H,res", [
+    (7001, 8, torch.bfloat16),       # one warp a row, more rows than CTAs: the stages go round
+    (9001, 256, torch.float32),
+    (5003, 520, torch.bfloat16),
+    (4001, 1032, torch.float32),
+    (2500, 2048, torch.bfloat16),
+])
+def test_backward_of_many_narrow_rows(T, H, res, gate):
+    a = make(T, H, res, gate, True, True, T + H)
+    got, dr_new, dn = run_backward(a, 0.7, EPS, T)
+    check_backward(a, got, dr_new, dn, 0.7, EPS)
+    again, _, _ = run_backward(a, 0.7, EPS, T)
+    for key, v in got.items():
+        assert v is None or torch.equal(v, again[key])

@@ -333,3 +333,145 @@ def test_ffn_output_in_the_place_of_its_input():
     lg = to_dev(np.random.default_rng(15).normal(size=(T, E)).astype(np.float32))
     want = nv.moe_ffn_w4a16(x, lg, k, w1, w2)
     assert torch.equal(nv.moe_ffn_w4a16(x, lg, k, w1, w2, out=x), want)
+
+
+# ------------------------------------------------- products with many output blocks, larger batches
+
+def random_weight(N, K, seed):
+    """Random codes and scales: (device weights, codes, scales, global scale)."""
+    rng = np.random.default_rng(seed)
+    codes = rng.integers(0, 16, (N, K), dtype=np.uint8)
+    sf = rng.integers(0x28, 0x41, (N, K // 16), dtype=np.uint8)  # 2^-2 to 2^1
+    gs = np.float32(37.5)
+    return raw_weight(codes, sf, gs), codes, sf, gs
+
+
+# (rows, N, K): one and two token tiles, one to four blocks of tokens, shares of a CTA that begin and end
+# inside blocks (but for K 64, a step per block), odd numbers of rows of the weight
+STREAMED = [(6, 531000, 64), (5, 265201, 320), (3, 65521, 2304), (9, 177003, 576),
+            (16, 110001, 1152), (33, 60001, 704), (64, 33333, 1280)]
+
+
+@pytest.mark.parametrize("M_,N,K", STREAMED)
+def test_linear_with_many_output_blocks(M_, N, K):
+    rows = (N + 127) // 128
+    # the form that streams the blocks in even shares: its workspace holds float32 planes of the output
+    assert nv.linear_w4a16_workspace_bytes(M_, N, K) >= M_ * rows * 128 * 4
+    w, codes, sf, gs = random_weight(N, K, seed=N)
+    rng = np.random.default_rng(M_)
+    wide = bf16(rng.normal(size=(2 * M_, K + 64)) * np.exp(rng.normal(size=(2 * M_, 1)) * 3)).to(DEV)
+    x = wide[1::2, 64:]
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = {t: nv.linear_w4a16(x, w, out_dtype=t, status=status) for t in (torch.float32, torch.bfloat16)}
+    again = nv.linear_w4a16(x, w, out_dtype=torch.float32)
+    assert nv.read_status(status) == (0, 0) and torch.equal(again, got[torch.float32])
+    x64 = x.double().cpu().numpy()
+    for n0 in range(0, N, 20000):
+        n = slice(n0, n0 + 20000)
+        ref, mag = P.linear(x64, Q.dequantize(codes[n], sf[n], gs))
+        for v in got.values():
+            check(v[:, n], ref, mag)
+
+
+@pytest.mark.parametrize("M_,N,K", [(1, 200, 512), (3, 200, 512), (12, 200, 512), (4, 265201, 320),
+                                    (34, 60001, 704)])
+def test_infinities_keep_their_sign_and_reach_every_output_of_the_row(M_, N, K):
+    w, codes, sf, gs = random_weight(N, K, seed=N + 1)
+    x = bf16(np.random.default_rng(2).normal(size=(M_, K)))
+    x[0, 3] = float("inf")
+    if M_ > 1:
+        x[1, K - 1], x[2] = float("nan"), 0.0
+    got = nv.linear_w4a16(x.to(DEV), w, out_dtype=torch.float32).cpu()
+    col = F.e2m1_decode(codes[:, 3])
+    # infinity times a weight of 0 is no number
+    want = torch.from_numpy(np.where(col == 0, np.nan, np.copysign(np.inf, col))).float()
+    assert torch.equal(torch.isnan(got[0]), torch.isnan(want))
+    ok = ~torch.isnan(want)
+    assert torch.equal(got[0][ok], want[ok])
+    if M_ > 1:
+        assert torch.isnan(got[1]).all() and (got[2] == 0).all()
+    for n0 in range(0, N, 20000):
+        n = slice(n0, n0 + 20000)
+        ref, mag = P.linear(x[3:].double().numpy(), Q.dequantize(codes[n], sf[n], gs))
+        check(got[3:, n], ref, mag)
+
+
+@pytest.mark.parametrize("M_,N,K", [(2, 531000, 64), (20, 90112, 704)])
+def test_streamed_linear_on_two_streams_and_in_a_graph(M_, N, K):
+    w, _, _, _ = random_weight(N, K, seed=7)
+    xs = [bf16(np.random.default_rng(s).normal(size=(M_, K))).to(DEV) for s in range(2)]
+    want = [nv.linear_w4a16(x, w) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(nv.linear_w4a16(xs[i], w))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert all(torch.equal(g, want[i]) for g in got[i])
+    ws = torch.full((nv.linear_w4a16_workspace_bytes(M_, N, K),), 0xFF, dtype=torch.uint8, device=DEV)
+    x = xs[0].clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=streams[0]):
+        out = nv.linear_w4a16(x, w, ws=ws)
+        again = nv.linear_w4a16(x, w, ws=ws)  # the same workspace, back to back
+    for i in (1, 0):
+        x.copy_(xs[i])
+        ws.fill_(0xFF)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[i]) and torch.equal(again, want[i])
+
+
+def share_of(T, I, E, k, ids, blocks, K):
+    """(steps of a block, steps of a CTA's share) of one of the FFN's products, as the kernels cut it."""
+    S, steps = T * k, (K + 255) // 256
+    tok = 8 if 2 * S // E <= 8 else 16
+    counts = np.bincount(ids[ids >= 0], minlength=E)
+    total = int(((counts + tok - 1) // tok).sum()) * blocks * steps
+    least = 4 if S <= 64 and steps > 4 else steps
+    return steps, max(least, -(-total // 296))
+
+
+@pytest.mark.parametrize("T,H,I,E,k", [
+    (9, 1152, 1152, 5, 2),     # few slots: shares of 4 steps of blocks of 5
+    (8, 1408, 640, 24, 8),     # 64 slots: shares of more steps than the ring has stages
+    (40, 640, 704, 48, 2),     # more slots, one token tile: shares longer than a block
+    (60, 640, 384, 64, 6),     # two token tiles
+])
+def test_ffn_shares_that_cross_blocks(T, H, I, E, k):
+    w1, w2, f1, f2 = make_experts(E, H, I, seed=T + E)
+    rng = np.random.default_rng(T)
+    x = bf16(rng.normal(size=(T, H)))
+    lg = rng.normal(size=(T, E)).astype(np.float32)
+    ids, wts = R.route_topk(lg, k)
+    steps, per = share_of(T, I, E, k, ids, 2 * I // 128, H)
+    assert per % steps and steps % per
+    got = nv.moe_ffn_w4a16(x.to(DEV), to_dev(lg), k, w1, w2)
+    check_ffn(got, x, ids, wts, f1, f2)
+    r = nv.permute(to_dev(lg), k)
+    assert torch.equal(got, nv.moe_ffn_w4a16(x.to(DEV), None, k, w1, w2, ids=r["ids"],
+                                             weights=r["weights"]))
+
+
+@pytest.mark.parametrize("T,E,k", [(512, 16, 8), (4096, 256, 1), (1500, 2, 2), (128, 32, 32)])
+def test_ffn_of_many_slots(T, E, k):
+    H, I = 128, 64
+    w1, w2, f1, f2 = make_experts(E, H, I, seed=T + E)
+    rng = np.random.default_rng(T)
+    x = bf16(rng.normal(size=(T, H)))
+    lg = rng.normal(size=(T, E)).astype(np.float32)
+    ids, wts = R.route_topk(lg, k)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = nv.moe_ffn_w4a16(x.to(DEV), to_dev(lg), k, w1, w2, status=status)
+    check_ffn(got, x, ids, wts, f1, f2)
+    # a given routing, with dropped slots and experts named twice by a token
+    ids = rng.integers(-1, E, size=(T, k)).astype(np.int32)
+    ids[T // 2:] = np.where(ids[T // 2:] >= 0, E - 1, -1)
+    wts = rng.uniform(0.1, 1, size=(T, k)).astype(np.float32)
+    got = nv.moe_ffn_w4a16(x.to(DEV), None, k, w1, w2, ids=to_dev(ids), weights=to_dev(wts),
+                           status=status)
+    check_ffn(got, x, ids, wts, f1, f2)
+    assert (got[(ids < 0).all(1)] == 0).all() and nv.read_status(status) == (0, 0)
