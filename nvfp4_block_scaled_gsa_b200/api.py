@@ -402,7 +402,8 @@ def linear_w4a16_workspace_bytes(M, N, K):
 
 def linear_w4a16(x, w: "NVFP4Weights", out_dtype=BF16, out=None, ws=None, status=None):
     """out (M, N) = x W^T with bf16 x (M, K) used as it is (not quantized, unlike linear()) and W
-    one NVFP4 matrix (w.E == 1): for up to a few dozen rows.  out_dtype bf16 or float32; any N,
+    one NVFP4 matrix (w.E == 1): for few rows (up to 8 of a large matrix, up to a few dozen of a
+    small one linear() is slower).  out_dtype bf16 or float32; any N,
     K % 64 == 0; a given out must not overlap x."""
     assert x.dtype == BF16 and x.dim() == 2 and x.stride(1) == 1 and w.E == 1
     assert out_dtype in (BF16, F32)

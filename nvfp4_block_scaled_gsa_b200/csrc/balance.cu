@@ -12,9 +12,10 @@
 // one pass over the logits gives both; no mean probability per expert is ever formed.  Two launches:
 // the counts from the ids (a cluster per sequence, its CTAs' histograms joined through distributed
 // shared memory, nothing to zero), and the pass, which loads its first logits while the counts
-// are still being made.  Bound by reading the logits and writing their gradient at many tokens (40961
-// x 160: 16.7 us, 3.0 TB/s, where the issue of its 180 instructions a token shows), and by
-// the chain of launches and dependent loads below (8192 x 256: 12.1 us, 64 x 8: 7 us).
+// are still being made.  Gradient of 40961 x 160: 20.0 us, 2.6 TB/s.  The schedulers issue in 63% of the
+// cycles in which an SM is busy (227 warp instructions a token), and what is left is the start, three
+// dependent loads, and the tail.  Below that the chain of launches and dependent loads is the bound
+// (8192 x 256 with the counts: 12.4 us, 64 x 8: 6.7 us; 40000 x 256 with the counts: 32.8 us).
 #include "common.cuh"
 #include "launch.h"
 
@@ -24,7 +25,10 @@ namespace {
 constexpr int kMaxE = 256;
 constexpr int kMaxK = 32;
 constexpr int kCountThreads = 512;
-constexpr int kCountCluster = 8;  // CTAs per sequence, up to kClusterSeqs sequences
+// CTAs per sequence, up to kClusterSeqs sequences, and one above: 40000 x 256 top-8 in 65 even sequences
+// 29.3 us with one CTA each against 33.6 with clusters, in 256 30.4 against 44.4.  One long sequence
+// among short ones would want the cluster (65: 52.2 us against 106), but the lengths are not known here.
+constexpr int kCountCluster = 8;
 constexpr int kClusterSeqs = 64;
 constexpr int kThreads = 256;
 // CTAs of the pass, at most: the 3 that an SM holds on each of the 148 (more than one round of
@@ -140,9 +144,9 @@ __device__ __forceinline__ float quotient(float a, float b, float y) {
 }
 
 // L lanes per token, 4 * NV logits each; a warp takes 32 / L consecutive tokens at a time.  Many
-// logits per lane keep the shuffles of the row sums few (40961 x 160 at 32 lanes of 8 was bound by
-// instruction issue, 297 a token: 18.4 us against 17.2 for the same arithmetic).  VEC: a lane's logits are NV 16-byte
-// groups (E % 4 == 0 and rows 16-byte aligned), else words L apart.
+// logits per lane keep the shuffles of the row sums few (40961 x 160 at 32 lanes of 8: 18.4 us against 17.2
+// for the same arithmetic, with a shorter exponential than today's).  VEC: a lane's logits are NV
+// 16-byte groups (E % 4 == 0 and rows 16-byte aligned), else words L apart.
 template <int L, int NV, bool VEC>
 __global__ void __launch_bounds__(kThreads, 3) balance_kernel(const Args A) {
   constexpr int G = 32 / L, kSlots = 4 * NV;

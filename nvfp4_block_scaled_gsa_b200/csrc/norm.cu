@@ -23,8 +23,8 @@
 // Both are bound by memory: 2 values of r and one each of y and n (forward), 3 of r, 2 of y and
 // one of n (backward) per element.  Forward, 8192 x 7168 with a float32 residual: 120 to 125 us, 5.6
 // to 5.9 TB/s (86 to 90% of a copy's rate; CTAs that stay and copy their next rows to shared memory
-// by themselves took 178).  Backward, 8191 x 7168 with the column sums: 167 us with a float32 residual
-// (97%), 141 us with a bf16 one (76%), where the same instructions meet fewer bytes: half of the issue
+// by themselves took 178); with a bf16 one 110 us (65%), waiting for loads with 28 warps an SM.  Backward,
+// 8191 x 7168 with the column sums: 167 us with a float32 residual (97%), 139 to 141 us with a bf16 one (76%), where the same instructions meet fewer bytes: half of the issue
 // slots are used and the rest goes to the one barrier per row, with the registers (128 x 512
 // threads, half of them column sums) allowing one CTA per SM.
 #include <atomic>

@@ -21,8 +21,8 @@
 // Exactness.  E2M1 * E4M3 has at most 6 significant bits and lies in [2^-10, 2688], so the
 // decoded weight is exact in f16.  A row of activations is multiplied by the power of two that
 // brings its largest finite magnitude into [2^14, 2^15): a bf16 value is then exact in f16 unless
-// it is below 2^-29 of that maximum, where it is off by at most 2^-40 of the maximum (less than
-// the float32 sum of K such products is off).  The FFN's float32 intermediate is rounded to f16's
+// it is below 2^-31 of that maximum, where it is off by at most 2^-39 of the maximum (half an f16
+// subnormal step is 2^-25; less than the float32 sum is off that the maximum takes part in).  The FFN's float32 intermediate is rounded to f16's
 // 11 bits there, 1/8 of the step that the bf16 output is rounded to in the end (a second f16 term
 // would double the MMAs, and they would be the bound).  Infinities and NaNs pass through the
 // conversion and the product as such.
