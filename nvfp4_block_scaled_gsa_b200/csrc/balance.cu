@@ -424,9 +424,7 @@ nvfp4_status_t check_shape(int T, int E, int k, int64_t ld, int S, const int32_t
 
 // Whether the gradient's rows lie over any of the logits, which other warps may still have to read.
 bool over_logits(const float* logits, int64_t ld, int T, int E, const float* dlogits) {
-  if (dlogits == nullptr || T == 0) return false;
-  const uintptr_t l = reinterpret_cast<uintptr_t>(logits), d = reinterpret_cast<uintptr_t>(dlogits);
-  return d < l + ((int64_t)(T - 1) * ld + E) * 4 && l < d + (int64_t)T * E * 4;
+  return rows_overlap(logits, T, ld * 4, (int64_t)E * 4, dlogits, (int64_t)T * E * 4);
 }
 
 }  // namespace

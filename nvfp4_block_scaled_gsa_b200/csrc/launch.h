@@ -10,6 +10,16 @@
 
 namespace nvfp4 {
 
+// Whether any of `rows` rows of `row` bytes, `pitch` bytes apart from `p` on, shares a byte with the `n`
+// bytes at `q`.  (What lies between the rows of a strided array is not part of it.)
+inline bool rows_overlap(const void* p, int64_t rows, int64_t pitch, int64_t row, const void* q, int64_t n) {
+  if (p == nullptr || q == nullptr || rows <= 0 || row <= 0 || n <= 0) return false;
+  const int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(q) - reinterpret_cast<uintptr_t>(p));
+  // the first row that ends behind q, and whether it begins before q's end
+  const int64_t first = d < row ? 0 : (d - row) / pitch + 1;
+  return first < rows && first * pitch < d + n;
+}
+
 nvfp4_status_t quantize_launch(const void* x, int64_t rows, int64_t cols, int64_t ld,
                                const int32_t* dst_row, int k, int64_t out_rows, uint8_t* codes,
                                uint8_t* sf, float* gs, int compute_gs, void* ws,

@@ -23,10 +23,11 @@
 // Both are bound by memory: 2 values of r and one each of y and n (forward), 3 of r, 2 of y and
 // one of n (backward) per element.  Forward, 8192 x 7168 with a float32 residual: 120 to 125 us, 5.6
 // to 5.9 TB/s (86 to 90% of a copy's rate; CTAs that stay and copy their next rows to shared memory
-// by themselves took 178); with a bf16 one 110 us (65%), waiting for loads with 28 warps an SM.  Backward,
-// 8191 x 7168 with the column sums: 167 us with a float32 residual (97%), 139 to 141 us with a bf16 one (76%), where the same instructions meet fewer bytes: half of the issue
-// slots are used and the rest goes to the one barrier per row, with the registers (128 x 512
-// threads, half of them column sums) allowing one CTA per SM.
+// by themselves took 178); with a bf16 one 110 us (65%), waiting for loads with 28 warps an SM.
+// Backward, 8191 x 7168 with the column sums: 167 us with a float32 residual (97%), 139 to 141 us with a
+// bf16 one (76%), where the same instructions meet fewer bytes: half of the issue slots are used and the
+// rest goes to the one barrier per row, with the registers (128 x 512 threads, half of them column
+// sums) allowing one CTA per SM.
 #include <atomic>
 
 #include "common.cuh"
@@ -666,35 +667,32 @@ nvfp4_status_t check_common(const Args& a, int r_dtype) {
   return NVFP4_OK;
 }
 
-// An array of a call, for the check of outputs that lie over something else: [T][H] in rows of `pitch`
-// elements, or a plain vector.
+// An array of a call, for the check of outputs that lie over something else: [T][H] in rows `pitch`
+// bytes apart, or a plain vector (one row, in no one's place).
 struct Span {
-  uintptr_t p, end;
-  int64_t pitch;  // 0: a vector
-  int size;       // of an element
+  const void* p;
+  int64_t rows, pitch, row;  // bytes
+  bool vector;
 };
 Span rows_span(const Args& a, const void* p, int size, int64_t pitch) {
-  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-  if (a.T == 1) pitch = a.H;
-  return {at, p == nullptr ? at : at + static_cast<uintptr_t>((a.T - 1) * pitch + a.H) * size, pitch, size};
+  return {p, a.T, a.T == 1 ? (int64_t)a.H * size : pitch * size, (int64_t)a.H * size, false};
 }
-Span vector_span(const void* p, int64_t n, int size) {
-  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-  return {at, p == nullptr ? at : at + static_cast<uintptr_t>(n) * size, 0, size};
-}
-// Outputs apart from one another and from the inputs.  Rows may take the place of the very same rows
-// (address, pitch and type): a row is read by the threads that write it, before they do.  Rows over
-// other rows would be written by one CTA while another still reads them.
+Span vector_span(const void* p, int64_t n, int size) { return {p, 1, n * size, n * size, true}; }
+// Outputs (dense) apart from one another and from the inputs.  Rows may take the place of the very same
+// rows (address, pitch and type): a row is read by the threads that write it, before they do.  Rows
+// over other rows would be written by one CTA while another still reads them.
 template <int O, int I>
 bool outputs_apart(const Span (&outs)[O], const Span (&ins)[I]) {
-  auto overlap = [](const Span& x, const Span& y) { return x.p < y.end && y.p < x.end; };
   for (int i = 0; i < O; ++i) {
     const Span& o = outs[i];
+    auto over = [&](const Span& x) {
+      return rows_overlap(x.p, x.rows, x.pitch, x.row, o.p, o.rows * o.row);
+    };
     for (int j = 0; j < i; ++j)
-      if (overlap(o, outs[j])) return false;
+      if (over(outs[j])) return false;
     for (const Span& in : ins)
-      if (overlap(o, in) &&
-          !(o.p == in.p && o.pitch != 0 && o.pitch == in.pitch && o.size == in.size))
+      if (over(in) &&
+          !(o.p == in.p && !o.vector && !in.vector && o.pitch == in.pitch && o.row == in.row))
         return false;
   }
   return true;

@@ -1282,9 +1282,8 @@ extern "C" nvfp4_status_t nvfp4_linear_w4a16(const void* x, int64_t M, int K, in
     return NVFP4_ERR_MISALIGNED;
   if (M == 0) return NVFP4_OK;
   // CTAs that have finished write rows of out while others still read x
-  const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), o0 = reinterpret_cast<uintptr_t>(out);
-  const uintptr_t x1 = x0 + ((M - 1) * ld + K) * 2, o1 = o0 + M * N * (out_dtype == 0 ? 4 : 2);
-  if (x0 < o1 && o0 < x1) return NVFP4_ERR_INVALID_ARG;
+  if (rows_overlap(x, M, ld * 2, (int64_t)K * 2, out, M * N * (out_dtype == 0 ? 4 : 2)))
+    return NVFP4_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(ws);
   int32_t* exps = reinterpret_cast<int32_t*>(base + P.exps);
@@ -1349,8 +1348,8 @@ extern "C" nvfp4_status_t moe_ffn_w4a16(const void* x_bf16, const float* logits,
   if (reinterpret_cast<uintptr_t>(ws) & 255u) return NVFP4_ERR_MISALIGNED;
   // CTAs that have finished write rows of out while others still read the weights (x and the ids are
   // read by the first kernel alone: out may be x)
-  const uintptr_t o0 = reinterpret_cast<uintptr_t>(out_bf16), w0 = reinterpret_cast<uintptr_t>(topk_w);
-  if (topk_w != nullptr && o0 < w0 + (int64_t)T * k * 4 && w0 < o0 + (int64_t)T * H * 2)
+  const int64_t w_bytes = (int64_t)T * k * 4;
+  if (rows_overlap(topk_w, 1, w_bytes, w_bytes, out_bf16, (int64_t)T * H * 2))
     return NVFP4_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(ws);

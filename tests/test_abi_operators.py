@@ -4,6 +4,8 @@ refusal before anything is launched."""
 import ctypes
 import os
 import re
+import subprocess
+import tempfile
 
 import pytest
 import torch
@@ -366,3 +368,32 @@ def test_residual_norm_takes_no_output_that_it_would_not_fill():
     x = torch.zeros(2, 64, dtype=torch.bfloat16)
     with pytest.raises(AssertionError, match="pre_gamma"):
         nv.residual_norm(x, x, out_n=torch.zeros_like(x))
+
+
+def test_overlap_of_strided_rows_is_exact():
+    # outputs between the rows of a strided input overlap nothing: compiled and run on the host
+    src = '''
+#include "launch.h"
+#include <stdio.h>
+int main() {
+  long long rows, pitch, row, at, n, bad = 0;
+  for (rows = 1; rows <= 4; ++rows) for (pitch = 4; pitch <= 9; ++pitch) for (row = 1; row <= pitch; ++row)
+  for (at = -12; at <= 40; ++at) for (n = 1; n <= 7; ++n) {
+    bool want = false;
+    for (long long r = 0; r < rows; ++r)
+      want = want || (r * pitch < at + n && at < r * pitch + row);
+    const char* p = reinterpret_cast<const char*>(1 << 20);
+    bad += nvfp4::rows_overlap(p, rows, pitch, row, p + at, n) != want;
+    bad += nvfp4::rows_overlap(nullptr, rows, pitch, row, p, n) || nvfp4::rows_overlap(p, rows, pitch, row, nullptr, n);
+  }
+  printf("%lld\\n", bad);
+}
+'''
+    with tempfile.TemporaryDirectory() as d:
+        with open(os.path.join(d, "t.cpp"), "w") as f:
+            f.write(src)
+        cuda = os.path.join(os.path.dirname(os.path.dirname(B.nvcc())), "include")
+        subprocess.run(["g++", "-std=c++17", "-I", B.CSRC, "-I", cuda, "-o", os.path.join(d, "t"),
+                        os.path.join(d, "t.cpp")], check=True)
+        out = subprocess.run([os.path.join(d, "t")], check=True, capture_output=True, text=True).stdout
+    assert out.strip() == "0"

@@ -352,3 +352,18 @@ def test_backward_of_many_narrow_rows(T, H, res, gate):
     again, _, _ = run_backward(a, 0.7, EPS, T)
     for key, v in got.items():
         assert v is None or torch.equal(v, again[key])
+
+
+def test_outputs_between_the_rows_of_strided_inputs():
+    a = make(3, 64, torch.bfloat16, "none", True, True, 6)
+    want = nv.residual_norm(**a, eps=EPS)
+    big = torch.zeros(3, 1024, dtype=torch.bfloat16, device=DEV)
+    big[:, :64] = a["r"]
+    a["r"] = big[:, :64]
+    out_r, out_n = big[0, 128:320].view(3, 64), big[1, 512:704].view(3, 64)
+    got = nv.residual_norm(**a, eps=EPS, out_r=out_r, out_n=out_n)
+    for g, w in zip(got, want):
+        assert torch.equal(g, w)
+    with pytest.raises(nv.Nvfp4Error):
+        nv.residual_norm(**a, eps=EPS, out_r=torch.empty_like(out_r),
+                         out_n=big.view(-1)[1024 - 128:1024 + 64].view(3, 64))
