@@ -579,7 +579,7 @@ NVFP4_API nvfp4_status_t moe_ffn_w4a16(const void* x_bf16, const float* logits,
  *          (S' = sequences with n_s > 0; 0 when there are none)
  *   dlogits_t[e] = dloss * alpha / (S' n_s) * p_t[e] * (f[s][e] - sum_j f[s][j] p_t[j])
  *   The counts are constants of the gradient.  A perfectly even load gives loss = alpha and a
- *   gradient of exactly 0.
+ *   gradient of exactly 0 (with up to 2^24 tokens in a sequence).
  *
  *   logits    float [T][ld] (ld >= E); a -inf logit has probability 0 and no gradient, a row of
  *             nothing but -inf has no probabilities at all (its token still counts in n_s)

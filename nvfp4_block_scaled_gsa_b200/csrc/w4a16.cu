@@ -22,10 +22,10 @@
 // decoded weight is exact in f16.  A row of activations is multiplied by the power of two that
 // brings its largest finite magnitude into [2^14, 2^15): a bf16 value is then exact in f16 unless
 // it is below 2^-31 of that maximum, where it is off by at most 2^-39 of the maximum (half an f16
-// subnormal step is 2^-25; less than the float32 sum is off that the maximum takes part in).  The FFN's float32 intermediate is rounded to f16's
-// 11 bits there, 1/8 of the step that the bf16 output is rounded to in the end (a second f16 term
-// would double the MMAs, and they would be the bound).  Infinities and NaNs pass through the
-// conversion and the product as such.
+// subnormal step is 2^-25; less than the float32 sum is off that the maximum takes part in).  The
+// FFN's float32 intermediate is rounded to f16's 11 bits there, 1/8 of the step that the bf16 output
+// is rounded to in the end (a second f16 term would double the MMAs, and they would be the bound).
+// Infinities and NaNs pass through the conversion and the product as such.
 //
 // Layout.  A warp owns 16 or 32 rows of a 128-row block, of which a lane's (g = lane/4) are 32
 // apart, and per step 256 elements of K, lane q = lane%4 the 64 elements from 64*q: 32 bytes of
